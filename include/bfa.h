@@ -295,6 +295,33 @@ bfa_status bfa_bwd(const bfa_plan* plan, const void* q, const void* k, const voi
                    const int64_t dk_strides[3], const int64_t dv_strides[3], void* stream);
 
 /*
+ * bfa_fwd and bfa_bwd with shaped scores:
+ *   z(i, j) = softcap * tanh(scale * q_i.k_j / softcap) - slopes[h] * |i - j|,
+ *   O = softmax(z + mask) V, LSE = log sum exp z over the attended keys,
+ * positions i, j local to the sequence, as the plan counts them (a key at the
+ * query's own position is at distance 0).
+ *   softcap: 0 for none, else in [1e-3, 1e6].  slopes: device f32 [H], one per
+ *   query head (any finite values), or NULL for no distance penalty.  With
+ *   softcap 0 and slopes NULL they are bfa_fwd and bfa_bwd.
+ * The backward takes the same shape as the forward whose out and lse it is given;
+ * the score gradient carries the cap's factor 1 - tanh^2; slopes are constants (no
+ * gradient).  Document, prefix, window and every other mask come from the plan;
+ * plans with GQA-packed tiles (bfa_plan_bsr_packed) are BFA_ERR_UNSUPPORTED (their
+ * tiles mix heads: plan the routing with bfa_plan_bsr).  Everything else as for
+ * bfa_fwd and bfa_bwd.
+ */
+bfa_status bfa_fwd_shaped(const bfa_plan* plan, const void* q, const void* k, const void* v,
+                          const int64_t q_strides[3], const int64_t k_strides[3], const int64_t v_strides[3],
+                          int B, int H, int Hkv, int D, float scale, float softcap, const float* slopes, void* out,
+                          const int64_t o_strides[3], float* lse, void* stream);
+bfa_status bfa_bwd_shaped(const bfa_plan* plan, const void* q, const void* k, const void* v, const void* out,
+                          const void* dout, const float* lse, const int64_t q_strides[3],
+                          const int64_t k_strides[3], const int64_t v_strides[3], const int64_t o_strides[3],
+                          const int64_t do_strides[3], int B, int H, int Hkv, int D, float scale, float softcap,
+                          const float* slopes, void* dq, void* dk, void* dv, const int64_t dq_strides[3],
+                          const int64_t dk_strides[3], const int64_t dv_strides[3], void* stream);
+
+/*
  * bfa_fwd with content-based block skipping (BinFlash approximate_softmax +
  * softmax_threshold, "BLASST-style"): once a query tile's scores are computed,
  * a key tile is dropped -- no exponentials, no P V product -- when every query
@@ -329,6 +356,83 @@ bfa_status bfa_fwd_paged(const bfa_plan* plan, const void* q, const int64_t q_st
                          const void* v_cache, const int64_t cache_strides[3], int64_t num_pages, int page_size,
                          const int32_t* block_table, int pages_per_seq, int B, int H, int Hkv, int D,
                          float scale, void* out, const int64_t o_strides[3], float* lse, void* stream);
+
+/*
+ * Attention of the newest tokens of each sequence over a paged cache, without a
+ * plan: single tokens (decoding), chunks of a prompt, or both in one batch.
+ *   q, out: bf16 [total_q, H, D] packed, strides {unused, token, head}; sequence s
+ *   owns rows cu_seqlens_q[s] .. cu_seqlens_q[s + 1] (device i32 [B + 1], starting
+ *   at 0).  Rows behind the last sequence are left as they are, in out and lse.
+ *   seqused_k: device i32 [B], keys of each sequence in the cache, the new tokens'
+ *   own included (append them first: bfa_append_paged).  New token t of a sequence
+ *   with n of them stands at position seqused_k - n + t and attends keys
+ *   0 <= j <= position, with window_left > 0 only position - j < window_left
+ *   (-1: no window).  Rows that attend nothing (an empty cache, a position below 0)
+ *   give out = 0 and lse = -inf.
+ *   k_cache, v_cache, cache_strides, num_pages, page_size, block_table,
+ *   pages_per_seq: as for bfa_fwd_paged.  Keys a sequence does not have, and keys
+ *   no new token sees, are not looked at (NaN there does no harm); lengths beyond
+ *   pages_per_seq * page_size count as that; page ids outside [0, num_pages) read
+ *   as keys and values of zeros.
+ *   max_q: the most new tokens of a sequence (0: unknown).  It only chooses the
+ *   tiles: sequences beyond it are served too.
+ *   scale, softcap, slopes: as for bfa_fwd_shaped.  lse: f32 [H, total_q] or NULL.
+ *   workspace: device, 16-byte aligned, at least bfa_fwd_chunk_workspace(...) bytes
+ *   for the same total_q, B, max_q, H, Hkv, D; its contents need no preparation
+ *   and are scratch until the call's work is done (calls that may overlap need one
+ *   each).
+ * All lengths and pages are read on the device: nothing is read back, the call
+ * never synchronises, and a captured call follows the arrays' contents at replay.
+ * Results do not depend on the order in which blocks run.
+ */
+int64_t bfa_fwd_chunk_workspace(int64_t total_q, int B, int max_q, int H, int Hkv, int D);
+bfa_status bfa_fwd_chunk(const void* q, const int64_t q_strides[3], const void* k_cache, const void* v_cache,
+                         const int64_t cache_strides[3], int64_t num_pages, int page_size,
+                         const int32_t* block_table, int pages_per_seq, const int32_t* cu_seqlens_q,
+                         const int32_t* seqused_k, int B, int64_t total_q, int max_q, int H, int Hkv, int D,
+                         float scale, int window_left, float softcap, const float* slopes, void* out,
+                         const int64_t o_strides[3], float* lse, void* workspace, int64_t workspace_bytes,
+                         void* stream);
+
+/*
+ * Rotary positions: pair (a, b) of a head at position n becomes
+ *   (amplitude * (a cos - b sin), amplitude * (a sin + b cos)),  angle n * inv_freq[i].
+ *   x, out: bf16 [B, S, H, D] (strides {batch, token, head}; packed [T, H, D] is
+ *   B = 1, S = T); out may be x itself.  inv_freq: device f64 [rotary / 2], radians
+ *   per position.  rotary: leading values of each head that turn, a multiple of 16
+ *   up to D; the rest is copied.  interleaved: pairs (2i, 2i + 1), else
+ *   (i, i + rotary / 2).  positions: device i32, or i64 with positions64, at
+ *   b * positions_batch_stride + s (stride 0: the same for every batch row); any
+ *   values, the angle is reduced in double.
+ *   inverse: the rotation by -angle (same amplitude), which is the gradient:
+ *   dx = bfa_rope(dout, inverse).
+ * Stream-ordered, no synchronisation.
+ */
+bfa_status bfa_rope(const void* x, const int64_t x_strides[3], void* out, const int64_t o_strides[3],
+                    const void* positions, int positions64, int64_t positions_batch_stride, const double* inv_freq,
+                    int rotary, int B, int64_t S, int H, int D, int interleaved, float amplitude, int inverse,
+                    void* stream);
+
+/*
+ * Write new keys and values into a paged cache, with rotary positions.
+ *   k, v: bf16 [total, Hkv, D] packed (strides {unused, token, head}), sequence s
+ *   owning rows cu_seqlens[s] .. cu_seqlens[s + 1]; seqused_k [B]: keys of each
+ *   sequence after the call, so that its token t of n lands at position
+ *   seqused_k - n + t, in the place that block_table gives (caches and table as for
+ *   bfa_fwd_chunk).  k turns by bfa_rope at that position (rotary 0: copied).
+ *   q [total, H, D], q_out: turned the same way in the same launch, or q NULL; q_out
+ *   may be q.  Tokens behind the last sequence are left out (their rows of q_out
+ *   stay as they are); tokens whose place does not exist (a position below 0 or
+ *   beyond pages_per_seq * page_size, a page id outside [0, num_pages)) are not
+ *   written.  Two tokens in one place: either may stay.
+ * Stream-ordered, no synchronisation.
+ */
+bfa_status bfa_append_paged(const void* k, const int64_t k_strides[3], const void* v, const int64_t v_strides[3],
+                            const void* q, const int64_t q_strides[3], void* q_out, const int64_t qo_strides[3],
+                            void* k_cache, void* v_cache, const int64_t cache_strides[3], int64_t num_pages,
+                            int page_size, const int32_t* block_table, int pages_per_seq, const int32_t* cu_seqlens,
+                            const int32_t* seqused_k, int B, int64_t total, int H, int Hkv, int D,
+                            const double* inv_freq, int rotary, int interleaved, float amplitude, void* stream);
 
 /* Host-side plan description (no sync). */
 bfa_status bfa_plan_get_info(const bfa_plan* plan, bfa_plan_info* info);

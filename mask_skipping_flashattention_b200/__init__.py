@@ -11,11 +11,18 @@ kernels.  There is no CPU path: CPU tensors are rejected by the library.
 Other mask sources: ``plan_blockids`` (opentau block ids, positions, varlen,
 sliding window) and ``plan_bsr`` (BSR routing); ``make_att_block_ids`` builds
 block ids from padding and block-opening flags.
+
+``fwd`` and ``bwd`` also take shaped scores (``softcap``, ``slopes``).  Beside the
+planned forms, ``fwd_chunk`` attends the newest tokens of each sequence over a
+paged cache (decoding included), ``append_paged`` fills that cache, and ``rope``
+(frequencies from ``rope_frequencies``) turns queries and keys by their positions.
 """
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
+import math
 
 import numpy as np
 import torch
@@ -26,6 +33,7 @@ from ._lib import BfaError, PlanInfo
 __all__ = ["Plan", "BfaError", "plan_dense", "plan_blockids", "plan_predicate", "plan_bsr", "plan_bsr_packed",
            "plan_block_bits",
            "fwd", "bwd", "fwd_paged",
+           "fwd_chunk", "append_paged", "rope", "rope_frequencies",
            "make_att_block_ids",
            "is_available", "load_error", "set_wait_timeout_ns", "set_bwd_deterministic", "selftest_wait_timeout", "library_path"]
 
@@ -43,6 +51,56 @@ def _stream(stream=None):
     if isinstance(stream, torch.cuda.Stream):
         return ctypes.c_void_p(stream.cuda_stream)
     return ctypes.c_void_p(int(stream))
+
+
+def _device_of(t):
+    """The device of ``t`` as the current one (CPU tensors are left to the library's refusal)."""
+    return torch.cuda.device(t.device) if t.is_cuda else contextlib.nullcontext()
+
+
+@contextlib.contextmanager
+def _launch_on(t, stream):
+    """The device of ``t`` and ``stream`` as the current ones, so that what is allocated inside
+    belongs to the stream that uses it; yields (stream handle, finish).  ``finish`` hands such
+    results back to the stream that was current."""
+    if not t.is_cuda:
+        yield _stream(stream), lambda *results: None
+        return
+    with torch.cuda.device(t.device):
+        ambient = torch.cuda.current_stream()
+        if stream is None:
+            yield _stream(), lambda *results: None
+            return
+        if not isinstance(stream, torch.cuda.Stream):
+            stream = torch.cuda.ExternalStream(int(stream), t.device) if int(stream) else torch.cuda.default_stream()
+        if stream.device != t.device:
+            raise ValueError(f"the stream is on {stream.device}, the tensors on {t.device}")
+
+        def finish(*results):
+            for r in results:
+                if r is not None and ambient != stream:
+                    r.record_stream(ambient)
+
+        with torch.cuda.stream(stream):
+            yield _stream(stream), finish
+
+
+def _same_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+
+
+def _score_shape(softcap, slopes, q, H):
+    """(softcap or 0, contiguous slopes or None), checked."""
+    if slopes is not None:
+        if slopes.dtype != torch.float32:
+            raise TypeError("slopes must be float32")
+        if slopes.shape != (H,):
+            raise ValueError(f"slopes must have one value per query head ({H}), not shape {tuple(slopes.shape)}")
+        _same_device(q, slopes)
+        slopes = slopes.contiguous()
+    return float(softcap) if softcap is not None else 0.0, slopes
 
 
 def _ptr(t):
@@ -318,13 +376,23 @@ def _strides3(t):
     raise ValueError("expected a 4-D (B, S, H, D) or 3-D (T, H, D) tensor")
 
 
-def fwd(plan, q, k, v, scale=None, out=None, return_lse=True, lse=None, stream=None, softmax_threshold=None):
+def fwd(plan, q, k, v, scale=None, out=None, return_lse=True, lse=None, stream=None, softmax_threshold=None,
+        softcap=None, slopes=None):
     """Masked attention forward; returns (out, lse or None).
 
     Batched q (B, Sq, H, D), k/v (B, Sk, Hkv, D); packed (varlen plans) q (Tq, H, D),
     k/v (Tk, Hkv, D).  bf16, last dim contiguous, D in {64, 128}.  A positive
     ``softmax_threshold`` turns on content-based block skipping (approximate).
+
+    Shaped scores: ``softcap * tanh(scale * q.k / softcap) - slopes[h] * |i - j|``, with
+    ``softcap`` in [1e-3, 1e6] (None: no cap) and ``slopes`` (H,) float32 (None: no
+    distance penalty); positions are those of the plan's masks.  Not with GQA-packed
+    plans or block skipping.
     """
+    if softcap is not None or slopes is not None:
+        if softmax_threshold is not None:
+            raise ValueError("softmax_threshold does not go with shaped scores")
+        return _fwd_shaped(plan, q, k, v, scale, out, return_lse, lse, stream, softcap, slopes)
     for t in (q, k, v):
         if t.dtype != torch.bfloat16:
             raise TypeError("q, k, v must be bfloat16")
@@ -359,13 +427,95 @@ def fwd(plan, q, k, v, scale=None, out=None, return_lse=True, lse=None, stream=N
     return out, lse
 
 
-def bwd(plan, q, k, v, out, dout, lse, scale=None, dq=None, dk=None, dv=None, stream=None):
+def _shapes(plan, q, k, v):
+    """(B, H, Hkv, D, lse shape) of a batched or packed call, with the forms and types checked."""
+    for t in (q, k, v):
+        if t.dtype != torch.bfloat16:
+            raise TypeError("q, k, v must be bfloat16")
+        if t.dim() != q.dim() or t.dim() not in (3, 4):
+            raise ValueError("q, k, v must all be (B, S, H, D) or all packed (T, H, D)")
+        if t.stride(-1) != 1:
+            raise ValueError("the head dim of q, k, v must be contiguous")
+    if k.shape != v.shape or k.shape[-1] != q.shape[-1]:
+        raise ValueError(f"q {tuple(q.shape)}, k {tuple(k.shape)} and v {tuple(v.shape)} do not fit together")
+    info = plan.info
+    if q.dim() == 3:
+        if not info["varlen"]:
+            raise ValueError("packed (T, H, D) tensors need a varlen plan")
+        B, lse_shape = info["batch"], (q.shape[1], q.shape[0])
+    else:
+        if info["varlen"]:
+            raise ValueError("a varlen plan needs packed (T, H, D) tensors")
+        B, lse_shape = q.shape[0], (q.shape[0], q.shape[2], q.shape[1])
+        if k.shape[0] != B:
+            raise ValueError("q and k must have the same batch size")
+    if q.shape[-3] != info["sq"] or k.shape[-3] != info["sk"]:
+        raise ValueError(f"the plan is for {info['sq']} queries and {info['sk']} keys, not {q.shape[-3]} and {k.shape[-3]}")
+    return int(B), int(q.shape[-2]), int(k.shape[-2]), int(q.shape[-1]), lse_shape
+
+
+def _result(t, like_shape, dtype, device, name):
+    """A caller's result tensor, checked, or a new one."""
+    if t is None:
+        return torch.empty(like_shape, dtype=dtype, device=device)
+    if tuple(t.shape) != tuple(like_shape) or t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be {tuple(like_shape)} {dtype} on {device}")
+    if t.dim() and t.stride(-1) != 1:
+        raise ValueError(f"the last dim of {name} must be contiguous")
+    return t
+
+
+def _fwd_shaped(plan, q, k, v, scale, out, return_lse, lse, stream, softcap, slopes):
+    B, H, Hkv, D, lse_shape = _shapes(plan, q, k, v)
+    _same_device(q, k, v)
+    cap, slopes = _score_shape(softcap, slopes, q, H)
+    if lse is not None and return_lse and not lse.is_contiguous():
+        raise ValueError("lse must be contiguous")
+    with _launch_on(q, stream) as (st, finish):
+        own_out, own_lse = out is None, lse is None
+        out = _result(out, q.shape, torch.bfloat16, q.device, "out")
+        lse = _result(lse, lse_shape, torch.float32, q.device, "lse") if return_lse else None
+        _lib.check(_L.bfa_fwd_shaped(plan.handle, _ptr(q), _ptr(k), _ptr(v), _strides3(q), _strides3(k), _strides3(v),
+                                     B, H, Hkv, D, ctypes.c_float(float(scale) if scale is not None else 0.0),
+                                     ctypes.c_float(cap), _ptr(slopes), _ptr(out), _strides3(out), _ptr(lse), st))
+        finish(out if own_out else None, lse if own_lse else None)
+    return out, lse
+
+
+def _bwd_shaped(plan, q, k, v, out, dout, lse, scale, dq, dk, dv, stream, softcap, slopes):
+    B, H, Hkv, D, lse_shape = _shapes(plan, q, k, v)
+    _same_device(q, k, v, out, dout, lse)
+    for t in (out, dout):
+        if t.dtype != torch.bfloat16 or t.shape != q.shape or t.stride(-1) != 1:
+            raise ValueError("out and dout must be bfloat16 with the shape of q and a contiguous head dim")
+    if lse is None or lse.dtype != torch.float32 or tuple(lse.shape) != tuple(lse_shape):
+        raise ValueError(f"lse (float32 {tuple(lse_shape)}, from fwd) is required")
+    cap, slopes = _score_shape(softcap, slopes, q, H)
+    with _launch_on(q, stream) as (st, finish):
+        own = [g is None for g in (dq, dk, dv)]
+        dq = _result(dq, q.shape, torch.bfloat16, q.device, "dq")
+        dk = _result(dk, k.shape, torch.bfloat16, q.device, "dk")
+        dv = _result(dv, v.shape, torch.bfloat16, q.device, "dv")
+        lse = lse.contiguous()
+        _lib.check(_L.bfa_bwd_shaped(plan.handle, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(dout), _ptr(lse),
+                                     _strides3(q), _strides3(k), _strides3(v), _strides3(out), _strides3(dout), B, H,
+                                     Hkv, D, ctypes.c_float(float(scale) if scale is not None else 0.0),
+                                     ctypes.c_float(cap), _ptr(slopes), _ptr(dq), _ptr(dk), _ptr(dv), _strides3(dq),
+                                     _strides3(dk), _strides3(dv), st))
+        finish(*(g for g, mine in zip((dq, dk, dv), own) if mine))
+    return dq, dk, dv
+
+
+def bwd(plan, q, k, v, out, dout, lse, scale=None, dq=None, dk=None, dv=None, stream=None, softcap=None, slopes=None):
     """Gradients (dq, dk, dv) of ``fwd`` for an upstream gradient ``dout`` of ``out``.
 
     q, k, v, the plan and scale exactly as given to ``fwd``; out and lse as it
     returned them; dout shaped like q.  bf16 outputs shaped like q, k, v (dk and
-    dv sum over the query heads of each kv head under GQA).
+    dv sum over the query heads of each kv head under GQA).  ``softcap`` and
+    ``slopes`` as given to ``fwd``; the slopes are constants, they get no gradient.
     """
+    if softcap is not None or slopes is not None:
+        return _bwd_shaped(plan, q, k, v, out, dout, lse, scale, dq, dk, dv, stream, softcap, slopes)
     for t in (q, k, v, out, dout):
         if t.dtype != torch.bfloat16:
             raise TypeError("q, k, v, out, dout must be bfloat16")
@@ -427,3 +577,197 @@ def fwd_paged(plan, q, k_cache, v_cache, block_table, scale=None, out=None, retu
                                 page_size, _ptr(bt), bt.shape[1], int(B), int(H), int(Hkv), int(D),
                                 ctypes.c_float(sc), _ptr(out), _strides3(out), _ptr(lse), _stream(stream)))
     return out, lse
+
+
+def _check_cache(k_cache, v_cache, block_table, cu_seqlens, seqused_k):
+    """(block_table, cu_seqlens, seqused_k) as contiguous int32, with the cache's form checked."""
+    if k_cache.dtype != torch.bfloat16 or v_cache.dtype != torch.bfloat16:
+        raise TypeError("the caches must be bfloat16")
+    if k_cache.dim() != 4 or k_cache.stride() != v_cache.stride() or k_cache.shape != v_cache.shape:
+        raise ValueError("k_cache and v_cache must be (num_pages, page_size, Hkv, D) with the same shape and strides")
+    if k_cache.stride(-1) != 1:
+        raise ValueError("the head dim of the caches must be contiguous")
+    B = seqused_k.numel()
+    if seqused_k.dim() != 1 or cu_seqlens.dim() != 1 or cu_seqlens.numel() != B + 1:
+        raise ValueError("cu_seqlens must hold one entry more than seqused_k")
+    if block_table.dim() != 2 or block_table.shape[0] != B:
+        raise ValueError("block_table must be (sequences, pages per sequence)")
+    ints = []
+    for t, name in ((block_table, "block_table"), (cu_seqlens, "cu_seqlens"), (seqused_k, "seqused_k")):
+        if t.dtype not in (torch.int32, torch.int64):
+            raise TypeError(f"{name} must be int32 or int64")
+        ints.append(t.to(torch.int32).contiguous())
+    _same_device(k_cache, v_cache, *ints)
+    return ints
+
+
+def _check_packed(t, name, heads, D):
+    if t.dtype != torch.bfloat16:
+        raise TypeError(f"{name} must be bfloat16")
+    if t.dim() != 3 or t.shape[2] != D or (heads is not None and t.shape[1] != heads):
+        raise ValueError(f"{name} must be (tokens, {'heads' if heads is None else heads}, {D}), not {tuple(t.shape)}")
+    if t.stride(-1) != 1:
+        raise ValueError(f"the head dim of {name} must be contiguous")
+
+
+def _cache_strides(c):
+    # a cache of one page has no page stride of its own
+    page = c.stride(0) if c.shape[0] > 1 else c.shape[1] * c.stride(1)
+    return (ctypes.c_int64 * 3)(page, c.stride(1), c.stride(2))
+
+
+def fwd_chunk(q, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, *, max_q=0, scale=None, window_left=-1,
+              softcap=None, slopes=None, out=None, return_lse=True, lse=None, workspace=None, stream=None):
+    """Attention of the newest tokens of each sequence over a paged cache; returns (out, lse or None).
+
+    q (T, H, D) bf16 packed by ``cu_seqlens_q`` (B + 1,); ``seqused_k`` (B,) keys of each
+    sequence, the new tokens' own included (``append_paged`` writes them).  The last
+    new token of a sequence stands at position seqused_k - 1; each attends the keys up
+    to its own position, of the last ``window_left`` of them if that is positive.
+    Caches and ``block_table`` as for ``fwd_paged``; ``softcap`` and ``slopes`` as for
+    ``fwd``.  ``max_q``: the most new tokens of a sequence, if known (it chooses tiles,
+    1 for decoding).  ``workspace``: a CUDA tensor to use as scratch, of at least
+    ``bfa_fwd_chunk_workspace`` bytes.  Lengths stay on the device: no synchronisation,
+    and a captured call follows their contents.  Rows of q behind the last sequence
+    are left as they are in out and lse.
+    """
+    block_table, cu, used = _check_cache(k_cache, v_cache, block_table, cu_seqlens_q, seqused_k)
+    num_pages, page_size, Hkv, D = k_cache.shape
+    _check_packed(q, "q", None, D)
+    _same_device(q, k_cache, workspace)
+    T, H, _ = q.shape
+    B = used.numel()
+    cap, slopes = _score_shape(softcap, slopes, q, H)
+    need = _L.bfa_fwd_chunk_workspace(T, B, int(max_q), H, Hkv, D)
+    if need < 0:
+        _lib.check(-2 if D not in (64, 128) else -1)
+    if lse is not None and return_lse and not lse.is_contiguous():
+        raise ValueError("lse must be contiguous")
+    with _launch_on(q, stream) as (st, finish):
+        own_out, own_lse = out is None, lse is None
+        out = _result(out, q.shape, torch.bfloat16, q.device, "out")
+        lse = _result(lse, (H, T), torch.float32, q.device, "lse") if return_lse else None
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        _lib.check(_L.bfa_fwd_chunk(_ptr(q), _strides3(q), _ptr(k_cache), _ptr(v_cache), _cache_strides(k_cache),
+                                    num_pages, page_size, _ptr(block_table), block_table.shape[1], _ptr(cu), _ptr(used),
+                                    B, T, int(max_q), H, Hkv, D,
+                                    ctypes.c_float(float(scale) if scale is not None else 0.0), int(window_left),
+                                    ctypes.c_float(cap), _ptr(slopes), _ptr(out), _strides3(out), _ptr(lse),
+                                    _ptr(workspace), workspace.numel() * workspace.element_size(), st))
+        finish(out if own_out else None, lse if own_lse else None)
+    return out, lse
+
+
+def rope_frequencies(rotary, base=10000.0, *, factor=1.0, ramp=None, device="cuda"):
+    """Radians per position of each pair, float64 (rotary / 2,): base ** (-2 i / rotary).
+
+    Long contexts: ``factor`` divides the frequencies (positions are interpolated).  With
+    ``ramp = (length, low, high)`` only slow pairs are divided: a pair that makes n turns
+    over ``length`` positions keeps the share clamp((n - low) / (high - low), 0, 1) of its
+    own frequency and takes the rest of the divided one.
+    """
+    if rotary <= 0 or rotary % 2:
+        raise ValueError("rotary must be a positive even number")
+    if not base > 0 or not factor > 0:
+        raise ValueError("base and factor must be positive")
+    f = torch.pow(torch.tensor(float(base), dtype=torch.float64),
+                  -torch.arange(0, rotary, 2, dtype=torch.float64) / rotary)
+    if ramp is None:
+        f = f / factor
+    else:
+        length, low, high = ramp
+        if not (length > 0 and high > low):
+            raise ValueError("ramp must be (length > 0, low, high > low)")
+        keep = ((length * f / (2 * math.pi) - low) / (high - low)).clamp(0, 1)
+        f = f * (keep + (1 - keep) / factor)
+    return f.to(device)
+
+
+def _check_frequencies(inv_freq, like):
+    if inv_freq is None:
+        return 0, None
+    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+        raise TypeError("inv_freq must be a 1-D float64 tensor (rope_frequencies)")
+    _same_device(like, inv_freq)
+    return 2 * inv_freq.numel(), inv_freq.contiguous()
+
+
+def rope(x, positions, inv_freq, *, interleaved=False, amplitude=1.0, inverse=False, out=None, stream=None):
+    """Rotary positions: x (B, S, H, D) or (T, H, D) bf16 with the first 2 * len(inv_freq)
+    values of each head turned in pairs; returns the result (``out=x`` works in place).
+
+    positions: int32 or int64, (B, S), or (S,) for every batch row, or (T,).  Pairs are
+    (i, i + rotary / 2), or (2 i, 2 i + 1) with ``interleaved``; ``amplitude`` scales
+    what turns.  ``inverse`` turns back: it is the gradient, dx = rope(dout, inverse=True).
+    """
+    if x.dtype != torch.bfloat16:
+        raise TypeError("x must be bfloat16")
+    if x.dim() not in (3, 4) or x.stride(-1) != 1:
+        raise ValueError("x must be (B, S, H, D) or (T, H, D) with a contiguous head dim")
+    if positions.dtype not in (torch.int32, torch.int64):
+        raise TypeError("positions must be int32 or int64")
+    B = x.shape[0] if x.dim() == 4 else 1
+    S, H, D = x.shape[-3:]
+    if positions.shape not in ((S,), x.shape[:-2]):
+        raise ValueError(f"positions must be {tuple(x.shape[:-2])} or {(S,)}, not {tuple(positions.shape)}")
+    rotary, inv_freq = _check_frequencies(inv_freq, x)
+    _same_device(x, positions)
+    positions = positions.contiguous()
+    if out is not None and out.data_ptr() == x.data_ptr() and out.stride() != x.stride():
+        raise ValueError("an in-place result must be x itself")
+    if x.numel() == 0:
+        return out if out is not None else torch.empty_like(x)
+    with _launch_on(x, stream) as (st, finish):
+        own_out = out is None
+        out = _result(out, x.shape, torch.bfloat16, x.device, "out")
+        _lib.check(_L.bfa_rope(_ptr(x), _strides3(x), _ptr(out), _strides3(out), _ptr(positions),
+                               1 if positions.dtype == torch.int64 else 0, S if positions.dim() == 2 else 0,
+                               _ptr(inv_freq), rotary, B, S, H, D, 1 if interleaved else 0,
+                               ctypes.c_float(float(amplitude)), 1 if inverse else 0, st))
+        finish(out if own_out else None)
+    return out
+
+
+def append_paged(k, v, k_cache, v_cache, block_table, cu_seqlens, seqused_k, *, q=None, q_out=None, inv_freq=None,
+                 interleaved=False, amplitude=1.0, stream=None):
+    """Write new keys and values (T, Hkv, D) into a paged cache, keys turned by their positions.
+
+    Sequence s owns rows cu_seqlens[s] .. cu_seqlens[s + 1]; ``seqused_k`` (B,) counts its
+    keys after the call.  ``q`` (T, H, D) is turned the same way in the same launch and
+    returned (into ``q_out``; ``q_out=q`` works in place); without q the result is None.
+    ``inv_freq`` None: keys and queries are copied.  Rows behind the last sequence are left
+    out.  Lengths and pages stay on the device, as for ``fwd_chunk``.
+    """
+    block_table, cu, used = _check_cache(k_cache, v_cache, block_table, cu_seqlens, seqused_k)
+    num_pages, page_size, Hkv, D = k_cache.shape
+    _check_packed(k, "k", Hkv, D)
+    _check_packed(v, "v", Hkv, D)
+    T, H = k.shape[0], Hkv
+    if v.shape != k.shape:
+        raise ValueError("k and v must have the same shape")
+    _same_device(k, v, k_cache, q)
+    if q is not None:
+        _check_packed(q, "q", None, D)
+        H = q.shape[1]
+        if q.shape[0] != T:
+            raise ValueError("q, k and v must hold the same tokens")
+        if q_out is not None and q_out.data_ptr() == q.data_ptr() and q_out.stride() != q.stride():
+            raise ValueError("an in-place q_out must be q itself")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    rotary, inv_freq = _check_frequencies(inv_freq, k)
+    with _launch_on(k, stream) as (st, finish):
+        own_out = q_out is None
+        if q is not None:
+            q_out = _result(q_out, q.shape, torch.bfloat16, q.device, "q_out")
+        none3 = (ctypes.c_int64 * 3)(0, 0, 0)
+        _lib.check(_L.bfa_append_paged(_ptr(k), _strides3(k), _ptr(v), _strides3(v), _ptr(q),
+                                       none3 if q is None else _strides3(q), _ptr(q_out),
+                                       none3 if q is None else _strides3(q_out), _ptr(k_cache), _ptr(v_cache),
+                                       _cache_strides(k_cache), num_pages, page_size, _ptr(block_table),
+                                       block_table.shape[1], _ptr(cu), _ptr(used), used.numel(), T, H, Hkv, D,
+                                       _ptr(inv_freq), rotary, 1 if interleaved else 0,
+                                       ctypes.c_float(float(amplitude)), st))
+        finish(q_out if own_out else None)
+    return q_out

@@ -61,6 +61,23 @@ SIGNATURES = {
     "bfa_fwd_paged": (ctypes.c_int, [c_void, c_void, c_i64p, c_void, c_void, c_i64p, ctypes.c_int64, ctypes.c_int,
                                      c_void, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                      ctypes.c_float, c_void, c_i64p, c_void, c_void]),
+    "bfa_fwd_shaped": (ctypes.c_int, [c_void, c_void, c_void, c_void, c_i64p, c_i64p, c_i64p, ctypes.c_int,
+                                      ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_float, ctypes.c_float,
+                                      c_void, c_void, c_i64p, c_void, c_void]),
+    "bfa_bwd_shaped": (ctypes.c_int, [c_void] * 7 + [c_i64p] * 5 + [ctypes.c_int] * 4 +
+                       [ctypes.c_float, ctypes.c_float, c_void, c_void, c_void, c_void] + [c_i64p] * 3 + [c_void]),
+    "bfa_fwd_chunk_workspace": (ctypes.c_int64, [ctypes.c_int64] + [ctypes.c_int] * 5),
+    "bfa_fwd_chunk": (ctypes.c_int, [c_void, c_i64p, c_void, c_void, c_i64p, ctypes.c_int64, ctypes.c_int, c_void,
+                                     ctypes.c_int, c_void, c_void, ctypes.c_int, ctypes.c_int64, ctypes.c_int,
+                                     ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_float, ctypes.c_int,
+                                     ctypes.c_float, c_void, c_void, c_i64p, c_void, c_void, ctypes.c_int64, c_void]),
+    "bfa_rope": (ctypes.c_int, [c_void, c_i64p, c_void, c_i64p, c_void, ctypes.c_int, ctypes.c_int64, c_void,
+                                ctypes.c_int, ctypes.c_int, ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                ctypes.c_float, ctypes.c_int, c_void]),
+    "bfa_append_paged": (ctypes.c_int, [c_void, c_i64p, c_void, c_i64p, c_void, c_i64p, c_void, c_i64p, c_void, c_void,
+                                        c_i64p, ctypes.c_int64, ctypes.c_int, c_void, ctypes.c_int, c_void, c_void,
+                                        ctypes.c_int, ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
+                                        c_void, ctypes.c_int, ctypes.c_int, ctypes.c_float, c_void]),
     "bfa_plan_get_info": (ctypes.c_int, [c_void, c_void]),
     "bfa_plan_stats": (ctypes.c_int, [c_void, c_i64p, c_i64p, c_i64p, c_void]),
     "bfa_plan_export": (ctypes.c_int, [c_void, c_void, c_void, c_void, c_void, c_void, c_void, c_void]),

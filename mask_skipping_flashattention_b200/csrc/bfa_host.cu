@@ -14,8 +14,10 @@
 
 #include "../../include/bfa.h"
 #include "bwd_params.cuh"
+#include "chunk_params.cuh"
 #include "fwd_params.cuh"
 #include "plan_types.cuh"
+#include "rope_params.cuh"
 
 #define BFA_API extern "C" __attribute__((visibility("default")))
 
@@ -996,6 +998,22 @@ int sm_count() {
   return n;
 }
 
+// cap and penalty of a call with softmax scale `scale` (softcap 0: none)
+ScoreParams score_params(float scale, float softcap, const float* slopes) {
+  ScoreParams sp;
+  sp.c0 = softcap > 0.f ? scale / softcap : 0.f;
+  sp.c1 = softcap > 0.f ? softcap * kLog2e : 0.f;
+  sp.slopes = slopes;
+  return sp;
+}
+
+// 0 (none) or within [1e-3, 1e6]
+bfa_status check_softcap(float softcap) {
+  if (softcap != 0.f && !(softcap >= 1e-3f && softcap <= 1e6f))
+    return fail(BFA_ERR_INVALID_ARG, "softcap=%g must be 0 (none) or between 1e-3 and 1e6", softcap);
+  return BFA_OK;
+}
+
 struct PagedKV {
   const int32_t* block_table = nullptr;
   int page_size = 0, pages_per_seq = 0;
@@ -1005,7 +1023,8 @@ struct PagedKV {
 cudaError_t fwd_launch_from_host(const bfa_plan* P, const void* q, const void* k, const void* v, const int64_t* qs,
                                  const int64_t* ks, const int64_t* vs, int B, int H, int Hkv, int D, float scale,
                                  void* out, const int64_t* os, float* lse, uint64_t wait_ns, cudaStream_t st,
-                                 std::string* why, const PagedKV& pg = PagedKV(), float skip_log2 = 0.f) {
+                                 std::string* why, const PagedKV& pg = PagedKV(), float skip_log2 = 0.f,
+                                 float softcap = 0.f, const float* slopes = nullptr) {
   const int bq = P->varlen ? 1 : B;
   const int G = P->pack_g;
   CUtensorMap tq, tk, tv, to;
@@ -1103,6 +1122,7 @@ cudaError_t fwd_launch_from_host(const bfa_plan* P, const void* q, const void* k
   p.page_size = pg.page_size;
   p.pages_per_seq = pg.pages_per_seq;
   p.skip_log2 = skip_log2;
+  p.score = score_params(sc, softcap, slopes);
   const int64_t n_work = units * items;
   return launch_fwd(D, tq, tk, tv, to, p, n_work, st);
 }
@@ -1113,7 +1133,8 @@ namespace {
 
 bfa_status fwd_checked(const bfa_plan* P, const void* q, const void* k, const void* v, const int64_t qs[3],
                        const int64_t ks[3], const int64_t vs[3], int B, int H, int Hkv, int D, float scale, void* out,
-                       const int64_t os[3], float* lse, void* stream, float skip_log2) {
+                       const int64_t os[3], float* lse, void* stream, float skip_log2, float softcap = 0.f,
+                       const float* slopes = nullptr) {
   if (!P) return fail(BFA_ERR_INVALID_ARG, "plan is NULL");
   if (!qs || !ks || !vs || !os) return fail(BFA_ERR_INVALID_ARG, "strides are NULL");
   if (D != 64 && D != 128) return fail(BFA_ERR_UNSUPPORTED, "head dim %d (supported: 64, 128)", D);
@@ -1139,7 +1160,7 @@ bfa_status fwd_checked(const bfa_plan* P, const void* q, const void* k, const vo
     if (reinterpret_cast<uintptr_t>(ptrs[t]) & 15u) return fail(BFA_ERR_INVALID_ARG, "tensor base is not 16-byte aligned");
   std::string why;
   cudaError_t e = fwd_launch_from_host(P, q, k, v, qs, ks, vs, B, H, Hkv, D, scale, out, os, lse, g_wait_ns,
-                                       static_cast<cudaStream_t>(stream), &why, PagedKV(), skip_log2);
+                                       static_cast<cudaStream_t>(stream), &why, PagedKV(), skip_log2, softcap, slopes);
   if (e != cudaSuccess) {
     if (!why.empty()) return fail(BFA_ERR_INVALID_ARG, "%s", why.c_str());
     return cuda_fail(e, "forward kernel");
@@ -1158,7 +1179,8 @@ bfa_status bwd_launch_from_host(bfa_plan* P, const void* q, const void* k, const
                                 const void* dout, const float* lse, const int64_t* qs, const int64_t* ks,
                                 const int64_t* vs, const int64_t* os, const int64_t* dos, int B, int H, int Hkv,
                                 int D, float scale, void* dq, void* dk, void* dv, const int64_t* dqs,
-                                const int64_t* dks, const int64_t* dvs, cudaStream_t st) {
+                                const int64_t* dks, const int64_t* dvs, cudaStream_t st, float softcap = 0.f,
+                                const float* slopes = nullptr) {
   std::string why;
   const int bq = P->varlen ? 1 : B;
   const int G = P->pack_g;
@@ -1259,6 +1281,7 @@ bfa_status bwd_launch_from_host(bfa_plan* P, const void* q, const void* k, const
   p.col_order = P->col_order;
   p.n_cols = n_cols;
   p.wait_ns = g_wait_ns;
+  p.score = score_params(sc, softcap, slopes);
   const int64_t ws_rows = static_cast<int64_t>(p.rep) * P->n_rows * kTile;
   // D = 128 runs the fused pass, which also needs the fp32 dQ sums (D floats a row),
   // unless reproducible sums were asked for
@@ -1293,13 +1316,21 @@ bfa_status bwd_launch_from_host(bfa_plan* P, const void* q, const void* k, const
   return BFA_OK;
 }
 
-}  // namespace
+// shaped scores: any plan but the GQA-packed ones, whose tiles mix heads
+bfa_status check_shaped(const bfa_plan* P, float softcap, const float* slopes) {
+  if (!P) return fail(BFA_ERR_INVALID_ARG, "plan is NULL");
+  if (P->pack_g > 1 && (softcap != 0.f || slopes))
+    return fail(BFA_ERR_UNSUPPORTED, "shaped scores need a plan without GQA-packed tiles (bfa_plan_bsr)");
+  const bfa_status s = check_softcap(softcap);
+  return s != BFA_OK ? s : need_device(slopes, "slopes", true);
+}
 
-BFA_API bfa_status bfa_bwd(const bfa_plan* Pc, const void* q, const void* k, const void* v, const void* out,
-                           const void* dout, const float* lse, const int64_t qs[3], const int64_t ks[3],
-                           const int64_t vs[3], const int64_t os[3], const int64_t dos[3], int B, int H, int Hkv,
-                           int D, float scale, void* dq, void* dk, void* dv, const int64_t dqs[3],
-                           const int64_t dks[3], const int64_t dvs[3], void* stream) {
+bfa_status bwd_checked(const bfa_plan* Pc, const void* q, const void* k, const void* v, const void* out,
+                       const void* dout, const float* lse, const int64_t qs[3], const int64_t ks[3],
+                       const int64_t vs[3], const int64_t os[3], const int64_t dos[3], int B, int H, int Hkv,
+                       int D, float scale, void* dq, void* dk, void* dv, const int64_t dqs[3],
+                       const int64_t dks[3], const int64_t dvs[3], void* stream, float softcap = 0.f,
+                       const float* slopes = nullptr) {
   if (!Pc) return fail(BFA_ERR_INVALID_ARG, "plan is NULL");
   bfa_plan* P = const_cast<bfa_plan*>(Pc);  // the transposed lists are a cache of the plan
   if (!qs || !ks || !vs || !os || !dos || !dqs || !dks || !dvs) return fail(BFA_ERR_INVALID_ARG, "strides are NULL");
@@ -1329,13 +1360,45 @@ BFA_API bfa_status bfa_bwd(const bfa_plan* Pc, const void* q, const void* k, con
   for (int t = 0; t < 8; ++t)
     if (reinterpret_cast<uintptr_t>(ptrs[t]) & 15u) return fail(BFA_ERR_INVALID_ARG, "tensor base is not 16-byte aligned");
   return bwd_launch_from_host(P, q, k, v, out, dout, lse, qs, ks, vs, os, dos, B, H, Hkv, D, scale, dq, dk, dv, dqs,
-                              dks, dvs, static_cast<cudaStream_t>(stream));
+                              dks, dvs, static_cast<cudaStream_t>(stream), softcap, slopes);
+}
+
+}  // namespace
+
+BFA_API bfa_status bfa_bwd(const bfa_plan* P, const void* q, const void* k, const void* v, const void* out,
+                           const void* dout, const float* lse, const int64_t qs[3], const int64_t ks[3],
+                           const int64_t vs[3], const int64_t os[3], const int64_t dos[3], int B, int H, int Hkv,
+                           int D, float scale, void* dq, void* dk, void* dv, const int64_t dqs[3],
+                           const int64_t dks[3], const int64_t dvs[3], void* stream) {
+  return bwd_checked(P, q, k, v, out, dout, lse, qs, ks, vs, os, dos, B, H, Hkv, D, scale, dq, dk, dv, dqs, dks, dvs,
+                     stream);
+}
+
+BFA_API bfa_status bfa_bwd_shaped(const bfa_plan* P, const void* q, const void* k, const void* v, const void* out,
+                                  const void* dout, const float* lse, const int64_t qs[3], const int64_t ks[3],
+                                  const int64_t vs[3], const int64_t os[3], const int64_t dos[3], int B, int H,
+                                  int Hkv, int D, float scale, float softcap, const float* slopes, void* dq, void* dk,
+                                  void* dv, const int64_t dqs[3], const int64_t dks[3], const int64_t dvs[3],
+                                  void* stream) {
+  bfa_status s = check_shaped(P, softcap, slopes);
+  if (s != BFA_OK) return s;
+  return bwd_checked(P, q, k, v, out, dout, lse, qs, ks, vs, os, dos, B, H, Hkv, D, scale, dq, dk, dv, dqs, dks, dvs,
+                     stream, softcap, slopes);
 }
 
 BFA_API bfa_status bfa_fwd(const bfa_plan* P, const void* q, const void* k, const void* v, const int64_t qs[3],
                            const int64_t ks[3], const int64_t vs[3], int B, int H, int Hkv, int D, float scale,
                            void* out, const int64_t os[3], float* lse, void* stream) {
   return fwd_checked(P, q, k, v, qs, ks, vs, B, H, Hkv, D, scale, out, os, lse, stream, 0.f);
+}
+
+BFA_API bfa_status bfa_fwd_shaped(const bfa_plan* P, const void* q, const void* k, const void* v,
+                                  const int64_t qs[3], const int64_t ks[3], const int64_t vs[3], int B, int H,
+                                  int Hkv, int D, float scale, float softcap, const float* slopes, void* out,
+                                  const int64_t os[3], float* lse, void* stream) {
+  bfa_status s = check_shaped(P, softcap, slopes);
+  if (s != BFA_OK) return s;
+  return fwd_checked(P, q, k, v, qs, ks, vs, B, H, Hkv, D, scale, out, os, lse, stream, 0.f, softcap, slopes);
 }
 
 BFA_API bfa_status bfa_fwd_approx(const bfa_plan* P, const void* q, const void* k, const void* v,
@@ -1401,6 +1464,287 @@ BFA_API bfa_status bfa_fwd_paged(const bfa_plan* P, const void* q, const int64_t
     if (!why.empty()) return fail(BFA_ERR_INVALID_ARG, "%s", why.c_str());
     return cuda_fail(e, "forward kernel");
   }
+  return BFA_OK;
+}
+
+// ----------------------------------------------------------------------------
+// chunks of new tokens over a paged cache, rotary positions, the cache's writer
+// ----------------------------------------------------------------------------
+namespace {
+
+// device memory of the current device, 16-byte aligned
+bfa_status need_here(const void* p, const char* name, bool allow_null = false) {
+  bfa_status s = need_device(p, name, allow_null);
+  if (s != BFA_OK || !p) return s;
+  cudaPointerAttributes a;
+  int dev = 0;
+  if (cudaPointerGetAttributes(&a, p) != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) {
+    cudaGetLastError();
+    return fail(BFA_ERR_NOT_DEVICE, "%s is not a device pointer", name);
+  }
+  if (a.type == cudaMemoryTypeDevice && a.device != dev)
+    return fail(BFA_ERR_INVALID_ARG, "%s is on device %d, the current device is %d", name, a.device, dev);
+  return BFA_OK;
+}
+
+bfa_status need_tensor(const void* p, const char* name, const int64_t* strides, bool batch) {
+  bfa_status s = need_here(p, name);
+  if (s != BFA_OK) return s;
+  if (!strides) return fail(BFA_ERR_INVALID_ARG, "strides of %s are NULL", name);
+  if (reinterpret_cast<uintptr_t>(p) & 15u) return fail(BFA_ERR_INVALID_ARG, "%s is not 16-byte aligned", name);
+  for (int i = batch ? 0 : 1; i < 3; ++i)
+    if (strides[i] < 0 || strides[i] % 8 != 0)
+      return fail(BFA_ERR_INVALID_ARG, "stride %lld of %s is not a non-negative multiple of 8 elements",
+                  (long long)strides[i], name);
+  return BFA_OK;
+}
+
+bfa_status check_heads(int H, int Hkv, int D) {
+  if (D != 64 && D != 128) return fail(BFA_ERR_UNSUPPORTED, "head dim %d (supported: 64, 128)", D);
+  if (H <= 0 || Hkv <= 0 || H % Hkv != 0)
+    return fail(BFA_ERR_INVALID_ARG, "H=%d must be a positive multiple of Hkv=%d", H, Hkv);
+  return BFA_OK;
+}
+
+// caches, page table and lengths of a ragged batch (the forms of bfa_fwd_paged)
+bfa_status check_cache(const void* k_cache, const void* v_cache, const int64_t* cs, int64_t num_pages, int page_size,
+                       const int32_t* block_table, int pages_per_seq, const int32_t* cu_seqlens,
+                       const int32_t* seqused_k, int B, int64_t total) {
+  if (!(page_size == 8 || page_size == 16 || page_size == 32 || page_size == 64 ||
+        (page_size > 0 && page_size % kTile == 0)))
+    return fail(BFA_ERR_INVALID_ARG, "page_size=%d must be 8, 16, 32, 64 or a multiple of 128", page_size);
+  if (num_pages <= 0 || pages_per_seq <= 0)
+    return fail(BFA_ERR_INVALID_ARG, "num_pages / pages_per_seq must be positive");
+  if (B <= 0) return fail(BFA_ERR_INVALID_ARG, "B=%d must be positive", B);
+  if (total < 0) return fail(BFA_ERR_INVALID_ARG, "total tokens must not be negative");
+  if (num_pages > (int64_t(1) << 31) / page_size || num_pages * page_size >= (int64_t(1) << 31))
+    return fail(BFA_ERR_CAPACITY, "cache too large");
+  if (static_cast<int64_t>(pages_per_seq) * page_size >= (int64_t(1) << 30))
+    return fail(BFA_ERR_CAPACITY, "pages_per_seq * page_size must stay below 2^30 keys");
+  bfa_status s;
+  if ((s = need_tensor(k_cache, "k_cache", cs, true)) || (s = need_tensor(v_cache, "v_cache", cs, true)) ||
+      (s = need_here(block_table, "block_table")) || (s = need_here(cu_seqlens, "cu_seqlens")) ||
+      (s = need_here(seqused_k, "seqused_k")))
+    return s;
+  if (cs[0] != static_cast<int64_t>(page_size) * cs[1])
+    return fail(BFA_ERR_INVALID_ARG, "cache pages must be contiguous (page stride = page_size * token stride)");
+  return BFA_OK;
+}
+
+// The split of a chunk call: which kernel serves it, with what row tiles, pieces
+// and workspace.
+struct ChunkSplit {
+  int row_tiles;             // 16-row blocks of a unit of the row kernel
+  int slots, min_tiles;
+  int64_t max_units, max_segs, bytes;
+};
+
+ChunkSplit chunk_split(int64_t total_q, int64_t B, int64_t max_q, int H, int Hkv, int D) {
+  ChunkSplit c;
+  const int64_t G = H / Hkv;
+  if (max_q <= 0 || max_q > total_q) max_q = total_q;
+  c.row_tiles = max_q * G <= 16 ? 1 : 2;
+  const int64_t R = 16 * c.row_tiles;
+  c.max_units = Hkv * (total_q * G / R + B);
+  c.slots = 8 * sm_count();
+  c.min_tiles = 4;
+  c.max_segs = c.max_units + c.slots;
+  c.bytes = c.max_segs * R * (static_cast<int64_t>(D) * 4 + 8);
+  return c;
+}
+
+}  // namespace
+
+BFA_API int64_t bfa_fwd_chunk_workspace(int64_t total_q, int B, int max_q, int H, int Hkv, int D) {
+  if (check_heads(H, Hkv, D) != BFA_OK) return -1;
+  if (total_q < 0 || B <= 0) {
+    fail(BFA_ERR_INVALID_ARG, "total_q must not be negative and B must be positive");
+    return -1;
+  }
+  return chunk_split(total_q, B, max_q, H, Hkv, D).bytes;
+}
+
+BFA_API bfa_status bfa_fwd_chunk(const void* q, const int64_t qs[3], const void* k_cache, const void* v_cache,
+                                 const int64_t cs[3], int64_t num_pages, int page_size, const int32_t* block_table,
+                                 int pages_per_seq, const int32_t* cu_seqlens_q, const int32_t* seqused_k, int B,
+                                 int64_t total_q, int max_q, int H, int Hkv, int D, float scale, int window_left,
+                                 float softcap, const float* slopes, void* out, const int64_t os[3], float* lse,
+                                 void* workspace, int64_t workspace_bytes, void* stream) {
+  bfa_status s;
+  if ((s = check_heads(H, Hkv, D)) || (s = check_softcap(softcap))) return s;
+  if (window_left == 0 || window_left < -1)
+    return fail(BFA_ERR_INVALID_ARG, "window_left=%d must be positive, or -1 for no window", window_left);
+  if ((s = check_cache(k_cache, v_cache, cs, num_pages, page_size, block_table, pages_per_seq, cu_seqlens_q, seqused_k,
+                       B, total_q)))
+    return s;
+  if (total_q == 0) return BFA_OK;
+  if ((s = need_tensor(q, "q", qs, false)) || (s = need_tensor(out, "out", os, false)) ||
+      (s = need_here(lse, "lse", true)) || (s = need_here(slopes, "slopes", true)))
+    return s;
+  const int G = H / Hkv;
+  const ChunkSplit c = chunk_split(total_q, B, max_q, H, Hkv, D);
+  if (total_q * G >= (int64_t(1) << 30) || c.max_segs >= (int64_t(1) << 31))
+    return fail(BFA_ERR_CAPACITY, "%lld query rows are too many for one call", (long long)(total_q * H));
+  if (workspace_bytes < c.bytes)
+    return fail(BFA_ERR_CAPACITY, "workspace of %lld bytes, %lld needed (bfa_fwd_chunk_workspace)",
+                (long long)workspace_bytes, (long long)c.bytes);
+  if ((s = need_here(workspace, "workspace"))) return s;
+  if (reinterpret_cast<uintptr_t>(workspace) & 15u)
+    return fail(BFA_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+  ChunkParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.D = D;
+  p.H = H;
+  p.Hkv = Hkv;
+  p.G = G;
+  p.B = B;
+  p.total_q = static_cast<int32_t>(total_q);
+  p.q = static_cast<const __nv_bfloat16*>(q);
+  p.q_ss = qs[1];
+  p.q_sh = qs[2];
+  p.out = static_cast<__nv_bfloat16*>(out);
+  p.o_ss = os[1];
+  p.o_sh = os[2];
+  p.lse = lse;
+  p.k_cache = static_cast<const __nv_bfloat16*>(k_cache);
+  p.v_cache = static_cast<const __nv_bfloat16*>(v_cache);
+  p.c_sp = cs[0];
+  p.c_st = cs[1];
+  p.c_sh = cs[2];
+  p.num_pages = num_pages;
+  p.page_size = page_size;
+  p.pages_per_seq = pages_per_seq;
+  p.block_table = block_table;
+  p.cu_seqlens = cu_seqlens_q;
+  p.seqused_k = seqused_k;
+  p.window = window_left < 0 ? -1 : std::min(window_left, 1 << 30);
+  const float sc = (scale > 0.f) ? scale : 1.0f / std::sqrt(static_cast<float>(D));
+  p.scale_log2 = sc * kLog2e;
+  p.score = score_params(sc, softcap, slopes);
+  p.rows_lo = 0;
+  p.rows_hi = INT64_MAX;
+  p.slots = c.slots;
+  p.min_tiles = c.min_tiles;
+  p.max_segs = static_cast<int32_t>(c.max_segs);
+  p.max_units = static_cast<int32_t>(c.max_units);
+  const int64_t R = 16 * c.row_tiles;
+  p.ws_o = static_cast<float*>(workspace);
+  p.ws_ml = reinterpret_cast<float2*>(p.ws_o + c.max_segs * R * D);
+  cudaError_t e = launch_chunk_rows(p, c.row_tiles, static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "chunk kernel");
+  return BFA_OK;
+}
+
+namespace {
+
+bfa_status check_rotary(const double* inv_freq, int rotary, int D, float amplitude, bool optional) {
+  if (rotary == 0 && optional) return BFA_OK;
+  if (rotary <= 0 || rotary > D || rotary % 16 != 0)
+    return fail(BFA_ERR_UNSUPPORTED, "rotary=%d must be a multiple of 16 up to the head dim %d", rotary, D);
+  if (!std::isfinite(amplitude)) return fail(BFA_ERR_INVALID_ARG, "amplitude must be finite");
+  return need_here(inv_freq, "inv_freq");
+}
+
+}  // namespace
+
+BFA_API bfa_status bfa_rope(const void* x, const int64_t xs[3], void* out, const int64_t os[3], const void* positions,
+                            int positions64, int64_t positions_batch_stride, const double* inv_freq, int rotary, int B,
+                            int64_t S, int H, int D, int interleaved, float amplitude, int inverse, void* stream) {
+  bfa_status s;
+  if ((s = check_heads(H, H, D))) return s;
+  if (B <= 0 || S < 0) return fail(BFA_ERR_INVALID_ARG, "B=%d must be positive and S=%lld not negative", B, (long long)S);
+  if (S == 0) return BFA_OK;
+  if (S >= (int64_t(1) << 31)) return fail(BFA_ERR_CAPACITY, "%lld tokens are too many for one call", (long long)S);
+  if (positions_batch_stride < 0) return fail(BFA_ERR_INVALID_ARG, "the positions' batch stride must not be negative");
+  if ((s = need_tensor(x, "x", xs, B > 1)) || (s = need_tensor(out, "out", os, B > 1)) ||
+      (s = need_here(positions, "positions")) || (s = check_rotary(inv_freq, rotary, D, amplitude, false)))
+    return s;
+  RopeParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.D = D;
+  p.rotary = rotary;
+  p.interleaved = interleaved ? 1 : 0;
+  p.amplitude = amplitude;
+  p.sign = inverse ? -1.f : 1.f;
+  p.inv_freq = inv_freq;
+  p.tokens = static_cast<int64_t>(B) * S;
+  p.S = static_cast<int32_t>(S);
+  p.H = H;
+  p.q = static_cast<const __nv_bfloat16*>(x);
+  p.q_sb = B > 1 ? xs[0] : 0;
+  p.q_ss = xs[1];
+  p.q_sh = xs[2];
+  p.q_out = static_cast<__nv_bfloat16*>(out);
+  p.qo_sb = B > 1 ? os[0] : 0;
+  p.qo_ss = os[1];
+  p.qo_sh = os[2];
+  p.positions = positions;
+  p.positions64 = positions64 ? 1 : 0;
+  p.pos_sb = positions_batch_stride;
+  p.page_size = 1;
+  cudaError_t e = launch_rope(p, sm_count(), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "rotary kernel");
+  return BFA_OK;
+}
+
+BFA_API bfa_status bfa_append_paged(const void* k, const int64_t ks[3], const void* v, const int64_t vs[3],
+                                    const void* q, const int64_t qs[3], void* q_out, const int64_t qos[3],
+                                    void* k_cache, void* v_cache, const int64_t cs[3], int64_t num_pages,
+                                    int page_size, const int32_t* block_table, int pages_per_seq,
+                                    const int32_t* cu_seqlens, const int32_t* seqused_k, int B, int64_t total, int H,
+                                    int Hkv, int D, const double* inv_freq, int rotary, int interleaved,
+                                    float amplitude, void* stream) {
+  bfa_status s;
+  if ((s = check_heads(q ? H : Hkv, Hkv, D)) ||
+      (s = check_cache(k_cache, v_cache, cs, num_pages, page_size, block_table, pages_per_seq, cu_seqlens, seqused_k, B,
+                       total)) ||
+      (s = check_rotary(inv_freq, rotary, D, amplitude, true)))
+    return s;
+  if (total == 0) return BFA_OK;
+  if (total >= (int64_t(1) << 31)) return fail(BFA_ERR_CAPACITY, "%lld tokens are too many for one call", (long long)total);
+  if ((s = need_tensor(k, "k", ks, false)) || (s = need_tensor(v, "v", vs, false)) ||
+      (q && ((s = need_tensor(q, "q", qs, false)) || (s = need_tensor(q_out, "q_out", qos, false)))))
+    return s;
+  RopeParams p;
+  std::memset(&p, 0, sizeof(p));
+  p.D = D;
+  p.rotary = rotary;
+  p.interleaved = interleaved ? 1 : 0;
+  p.amplitude = amplitude;
+  p.sign = 1.f;
+  p.inv_freq = inv_freq;
+  p.tokens = total;
+  p.S = static_cast<int32_t>(total);
+  p.H = q ? H : 0;
+  p.Hkv = Hkv;
+  if (q) {
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.q_ss = qs[1];
+    p.q_sh = qs[2];
+    p.q_out = static_cast<__nv_bfloat16*>(q_out);
+    p.qo_ss = qos[1];
+    p.qo_sh = qos[2];
+  }
+  p.cu_seqlens = cu_seqlens;
+  p.seqused_k = seqused_k;
+  p.n_seq = B;
+  p.k = static_cast<const __nv_bfloat16*>(k);
+  p.k_ss = ks[1];
+  p.k_sh = ks[2];
+  p.v = static_cast<const __nv_bfloat16*>(v);
+  p.v_ss = vs[1];
+  p.v_sh = vs[2];
+  p.k_cache = static_cast<__nv_bfloat16*>(k_cache);
+  p.v_cache = static_cast<__nv_bfloat16*>(v_cache);
+  p.c_sp = cs[0];
+  p.c_st = cs[1];
+  p.c_sh = cs[2];
+  p.num_pages = num_pages;
+  p.page_size = page_size;
+  p.pages_per_seq = pages_per_seq;
+  p.block_table = block_table;
+  cudaError_t e = launch_rope(p, sm_count(), static_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "append kernel");
   return BFA_OK;
 }
 

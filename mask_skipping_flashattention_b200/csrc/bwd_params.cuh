@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include "plan_types.cuh"
+#include "score.cuh"
 
 namespace bfa {
 
@@ -54,6 +55,7 @@ struct BwdParams {
   const int32_t* col_order;
   int32_t n_cols;
   uint64_t wait_ns;
+  ScoreParams score;  // tanh cap and distance penalty (the kScore instances)
 };
 
 cudaError_t launch_bwd_prep(const BwdParams& p, cudaStream_t s);

@@ -33,10 +33,12 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "device_once.cuh"
 #include "fwd_params.cuh"
 #include "plan_types.cuh"
 #include "pred.cuh"
 #include "ptx.cuh"
+#include "score.cuh"
 #include "tile_mask.cuh"
 
 namespace bfa {
@@ -272,8 +274,10 @@ __device__ __forceinline__ void issue_pv(uint32_t tO, uint32_t tP, uint8_t* sV, 
 
 // kSkip: approximate mode (content-based block skipping); the exact kernel is
 // compiled without any of its code.  kPacked: GQA-packed query tiles (5-D Q / O
-// boxes, rows mapped to (position, head)); the other kernels hold none of it.
-template <int D, bool kSkip, bool kPacked>
+// boxes, rows mapped to (position, head)); kScore: shaped scores (score.cuh), which
+// the softmax warps make of S right after they load it, so that the rest of the
+// loop is the plain kernel's with a scale of 1; the other kernels hold none of it.
+template <int D, bool kSkip, bool kPacked, bool kScore>
 __global__ void __launch_bounds__(kThreads, 1)
     bfa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
@@ -458,7 +462,11 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int n = slot ? wk.n[1] : wk.n[0];
       const int e0 = slot ? wk.e0[1] : wk.e0[0];
       const int qpos = (slot ? wk.qt[1] : wk.qt[0]) * kTile + row;  // position of this row inside its group
-      const float c = p.scale_log2;
+      const float c = kScore ? 1.f : p.scale_log2;
+      float slope = 0.f;
+      if constexpr (kScore) {
+        if (p.score.slopes) slope = __ldg(p.score.slopes + (slot ? wk.h[1] : wk.h[0])) * kLog2e;
+      }
       float m = -INFINITY, l = 0.f;
       bool ok = true;
       int kt_next = n > 0 ? p.plan.kv_tile[e0] : 0;
@@ -491,6 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
         reg_fence(sr);
         float* s = reinterpret_cast<float*>(sr);
+        if constexpr (kScore) shape_row(s, p.score, p.scale_log2, slope, qpos - kt * kTile);
         if (masked) {
 #pragma unroll
           for (int j = 0; j < 128; ++j)
@@ -708,13 +717,15 @@ static cudaError_t prepare(K kernel, int smem) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 
-template <int D, bool kSkip, bool kPacked>
+template <int D, bool kSkip, bool kPacked, bool kScore = false>
 static cudaError_t launch_one(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                               const CUtensorMap& to, const FwdParams& p, int64_t n_work, cudaStream_t s) {
-  static cudaError_t ready = prepare(bfa_fwd_kernel<D, kSkip, kPacked>, Cfg<D>::kSmemBytes);
+  static DeviceOnce once;
+  const cudaError_t ready =
+      once.run([] { return prepare(bfa_fwd_kernel<D, kSkip, kPacked, kScore>, Cfg<D>::kSmemBytes); });
   if (ready != cudaSuccess) return ready;
-  bfa_fwd_kernel<D, kSkip, kPacked><<<static_cast<unsigned>(n_work), kThreads, Cfg<D>::kSmemBytes, s>>>(tq, tk, tv,
-                                                                                                       to, p);
+  bfa_fwd_kernel<D, kSkip, kPacked, kScore>
+      <<<static_cast<unsigned>(n_work), kThreads, Cfg<D>::kSmemBytes, s>>>(tq, tk, tv, to, p);
   return cudaGetLastError();
 }
 
@@ -722,6 +733,10 @@ template <int D>
 static cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                             const CUtensorMap& to, const FwdParams& p, int64_t n_work, cudaStream_t s) {
   const bool approx = p.skip_log2 > 0.f, packed = p.pack_g > 1;
+  if (p.score.c1 != 0.f || p.score.slopes) {  // the host refuses these with packed plans or skipping
+    if (packed || approx) return cudaErrorInvalidValue;
+    return launch_one<D, false, false, true>(tq, tk, tv, to, p, n_work, s);
+  }
   if (packed)
     return approx ? launch_one<D, true, true>(tq, tk, tv, to, p, n_work, s)
                   : launch_one<D, false, true>(tq, tk, tv, to, p, n_work, s);
@@ -743,12 +758,14 @@ cudaError_t launch_wait_selftest(uint32_t* err, uint64_t cap, cudaStream_t s) {
 
 cudaError_t probe_fwd_kernels() {
   cudaFuncAttributes a;
-  cudaError_t e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<128, false, false>);
-  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<64, false, false>);
-  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<128, true, false>);
-  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<64, true, false>);
-  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<128, false, true>);
-  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<64, false, true>);
+  cudaError_t e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<128, false, false, false>);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<64, false, false, false>);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<128, true, false, false>);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<64, true, false, false>);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<128, false, true, false>);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<64, false, true, false>);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<128, false, false, true>);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<64, false, false, true>);
   return e;
 }
 

@@ -7,6 +7,7 @@
 #include <cuda_runtime.h>
 
 #include "plan_types.cuh"
+#include "score.cuh"
 
 namespace bfa {
 
@@ -37,6 +38,7 @@ struct FwdParams {
   // 5-D maps.  pack_g = 1: rows are positions of one head.
   int32_t pack_g;
   int32_t pack_shift;
+  ScoreParams score;  // tanh cap and distance penalty (the kScore instances)
 };
 
 int fwd_smem_bytes(int D);
