@@ -307,7 +307,9 @@ bfa_status bfa_bwd(const bfa_plan* plan, const void* q, const void* k, const voi
  * the score gradient carries the cap's factor 1 - tanh^2; slopes are constants (no
  * gradient).  Document, prefix, window and every other mask come from the plan;
  * plans with GQA-packed tiles (bfa_plan_bsr_packed) are BFA_ERR_UNSUPPORTED (their
- * tiles mix heads: plan the routing with bfa_plan_bsr).  Everything else as for
+ * tiles mix heads: plan the routing with bfa_plan_bsr), and so is a tensor that
+ * repeats its data along an axis (stride 0).  Keys and values that nothing attends
+ * are multiplied by weights of 0, so they must be finite.  Everything else as for
  * bfa_fwd and bfa_bwd.
  */
 bfa_status bfa_fwd_shaped(const bfa_plan* plan, const void* q, const void* k, const void* v,
@@ -383,7 +385,10 @@ bfa_status bfa_fwd_paged(const bfa_plan* plan, const void* q, const int64_t q_st
  *   each).
  * All lengths and pages are read on the device: nothing is read back, the call
  * never synchronises, and a captured call follows the arrays' contents at replay.
- * Results do not depend on the order in which blocks run.
+ * Results do not depend on the order in which blocks run.  A wait that gives up
+ * (bfa_set_wait_timeout_ns) is reported by bfa_chunk_device_status, which
+ * synchronises `stream`, covers every chunk call on the current device since it
+ * was last asked, and clears what it reports.
  */
 int64_t bfa_fwd_chunk_workspace(int64_t total_q, int B, int max_q, int H, int Hkv, int D);
 bfa_status bfa_fwd_chunk(const void* q, const int64_t q_strides[3], const void* k_cache, const void* v_cache,
@@ -393,6 +398,7 @@ bfa_status bfa_fwd_chunk(const void* q, const int64_t q_strides[3], const void* 
                          float scale, int window_left, float softcap, const float* slopes, void* out,
                          const int64_t o_strides[3], float* lse, void* workspace, int64_t workspace_bytes,
                          void* stream);
+bfa_status bfa_chunk_device_status(void* stream);
 
 /*
  * Rotary positions: pair (a, b) of a head at position n becomes

@@ -33,7 +33,7 @@ from ._lib import BfaError, PlanInfo
 __all__ = ["Plan", "BfaError", "plan_dense", "plan_blockids", "plan_predicate", "plan_bsr", "plan_bsr_packed",
            "plan_block_bits",
            "fwd", "bwd", "fwd_paged",
-           "fwd_chunk", "append_paged", "rope", "rope_frequencies",
+           "fwd_chunk", "chunk_device_status", "append_paged", "rope", "rope_frequencies",
            "make_att_block_ids",
            "is_available", "load_error", "set_wait_timeout_ns", "set_bwd_deterministic", "selftest_wait_timeout", "library_path"]
 
@@ -657,6 +657,11 @@ def fwd_chunk(q, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, *, max_
                                     _ptr(workspace), workspace.numel() * workspace.element_size(), st))
         finish(out if own_out else None, lse if own_lse else None)
     return out, lse
+
+
+def chunk_device_status(stream=None):
+    """Raise BfaError(BFA_ERR_TIMEOUT) if a ``fwd_chunk`` on the current device hit its wait bound."""
+    _lib.check(_L.bfa_chunk_device_status(_stream(stream)))
 
 
 def rope_frequencies(rotary, base=10000.0, *, factor=1.0, ramp=None, device="cuda"):

@@ -71,6 +71,7 @@ SIGNATURES = {
                                      ctypes.c_int, c_void, c_void, ctypes.c_int, ctypes.c_int64, ctypes.c_int,
                                      ctypes.c_int, ctypes.c_int, ctypes.c_int, ctypes.c_float, ctypes.c_int,
                                      ctypes.c_float, c_void, c_void, c_i64p, c_void, c_void, ctypes.c_int64, c_void]),
+    "bfa_chunk_device_status": (ctypes.c_int, [c_void]),
     "bfa_rope": (ctypes.c_int, [c_void, c_i64p, c_void, c_i64p, c_void, ctypes.c_int, ctypes.c_int64, c_void,
                                 ctypes.c_int, ctypes.c_int, ctypes.c_int64, ctypes.c_int, ctypes.c_int, ctypes.c_int,
                                 ctypes.c_float, ctypes.c_int, c_void]),

@@ -20,9 +20,9 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbfa.so")
 LIB_CHECKED = os.path.join(PKG, "libbfa_checked.so")
-SOURCES = ["planner.cu", "fwd.cu", "bwd.cu", "chunk.cu", "rope.cu", "bfa_host.cu"]
+SOURCES = ["planner.cu", "fwd.cu", "bwd.cu", "chunk.cu", "chunk_tile.cu", "rope.cu", "bfa_host.cu"]
 HEADERS = ["ptx.cuh", "plan_types.cuh", "fwd_params.cuh", "pred.cuh", "tile_mask.cuh", "bwd_params.cuh",
-           "score.cuh", "chunk_params.cuh", "chunk_split.cuh", "rope_params.cuh", "device_once.cuh"]
+           "fwd_tiles.cuh", "score.cuh", "chunk_params.cuh", "chunk_split.cuh", "rope_params.cuh", "device_once.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-fvisibility=hidden", "-Xptxas", "-v",
          f"-I{os.path.join(ROOT, 'include')}"]

@@ -1325,6 +1325,15 @@ bfa_status check_shaped(const bfa_plan* P, float softcap, const float* slopes) {
   return s != BFA_OK ? s : need_device(slopes, "slopes", true);
 }
 
+// The tensor maps of the planned kernels have no stride 0: an axis that repeats its
+// data (an expanded tensor) would be read as a contiguous one.
+bfa_status check_repeats(const bfa_plan* P, const int64_t* strides, const char* name, int B, int heads, int tokens) {
+  if (!strides) return BFA_OK;  // refused later
+  if ((!P->varlen && B > 1 && strides[0] == 0) || (tokens > 1 && strides[1] == 0) || (heads > 1 && strides[2] == 0))
+    return fail(BFA_ERR_UNSUPPORTED, "%s repeats its data along an axis (stride 0): make it contiguous", name);
+  return BFA_OK;
+}
+
 bfa_status bwd_checked(const bfa_plan* Pc, const void* q, const void* k, const void* v, const void* out,
                        const void* dout, const float* lse, const int64_t qs[3], const int64_t ks[3],
                        const int64_t vs[3], const int64_t os[3], const int64_t dos[3], int B, int H, int Hkv,
@@ -1380,8 +1389,12 @@ BFA_API bfa_status bfa_bwd_shaped(const bfa_plan* P, const void* q, const void* 
                                   int Hkv, int D, float scale, float softcap, const float* slopes, void* dq, void* dk,
                                   void* dv, const int64_t dqs[3], const int64_t dks[3], const int64_t dvs[3],
                                   void* stream) {
-  bfa_status s = check_shaped(P, softcap, slopes);
-  if (s != BFA_OK) return s;
+  bfa_status s;
+  if ((s = check_shaped(P, softcap, slopes)) || (s = check_repeats(P, qs, "q", B, H, P->sq)) ||
+      (s = check_repeats(P, ks, "k", B, Hkv, P->sk)) || (s = check_repeats(P, vs, "v", B, Hkv, P->sk)) ||
+      (s = check_repeats(P, dos, "dout", B, H, P->sq)) || (s = check_repeats(P, dqs, "dq", B, H, P->sq)) ||
+      (s = check_repeats(P, dks, "dk", B, Hkv, P->sk)) || (s = check_repeats(P, dvs, "dv", B, Hkv, P->sk)))
+    return s;
   return bwd_checked(P, q, k, v, out, dout, lse, qs, ks, vs, os, dos, B, H, Hkv, D, scale, dq, dk, dv, dqs, dks, dvs,
                      stream, softcap, slopes);
 }
@@ -1396,8 +1409,11 @@ BFA_API bfa_status bfa_fwd_shaped(const bfa_plan* P, const void* q, const void* 
                                   const int64_t qs[3], const int64_t ks[3], const int64_t vs[3], int B, int H,
                                   int Hkv, int D, float scale, float softcap, const float* slopes, void* out,
                                   const int64_t os[3], float* lse, void* stream) {
-  bfa_status s = check_shaped(P, softcap, slopes);
-  if (s != BFA_OK) return s;
+  bfa_status s;
+  if ((s = check_shaped(P, softcap, slopes)) || (s = check_repeats(P, qs, "q", B, H, P->sq)) ||
+      (s = check_repeats(P, ks, "k", B, Hkv, P->sk)) || (s = check_repeats(P, vs, "v", B, Hkv, P->sk)) ||
+      (s = check_repeats(P, os, "out", B, H, P->sq)))
+    return s;
   return fwd_checked(P, q, k, v, qs, ks, vs, B, H, Hkv, D, scale, out, os, lse, stream, 0.f, softcap, slopes);
 }
 
@@ -1470,6 +1486,9 @@ BFA_API bfa_status bfa_fwd_paged(const bfa_plan* P, const void* q, const int64_t
 // ----------------------------------------------------------------------------
 // chunks of new tokens over a paged cache, rotary positions, the cache's writer
 // ----------------------------------------------------------------------------
+// status word of the chunk kernels, one a device (they have no plan to hold it)
+static __device__ uint32_t g_chunk_err;
+
 namespace {
 
 // device memory of the current device, 16-byte aligned
@@ -1528,29 +1547,55 @@ bfa_status check_cache(const void* k_cache, const void* v_cache, const int64_t* 
     return s;
   if (cs[0] != static_cast<int64_t>(page_size) * cs[1])
     return fail(BFA_ERR_INVALID_ARG, "cache pages must be contiguous (page stride = page_size * token stride)");
+  if (cs[1] == 0 || cs[2] == 0)
+    return fail(BFA_ERR_INVALID_ARG, "the caches' token and head strides must be positive");
   return BFA_OK;
 }
 
-// The split of a chunk call: which kernel serves it, with what row tiles, pieces
-// and workspace.
-struct ChunkSplit {
-  int row_tiles;             // 16-row blocks of a unit of the row kernel
-  int slots, min_tiles;
-  int64_t max_units, max_segs, bytes;
+// The split of a chunk call.  Sequences with up to kRowKernelRows query rows a kv
+// head go to the row kernel, longer ones to the tile kernel; a call whose max_q
+// rules one of them out launches only the other, which then serves every sequence.
+constexpr int64_t kRowKernelRows = 64;
+
+struct ChunkPart {
+  int rows = 0;  // rows of a unit (0: not launched)
+  int slots = 0, min_tiles = 0;
+  int64_t max_units = 0, max_segs = 0, bytes = 0;
 };
+struct ChunkSplit {
+  ChunkPart row, tile;
+  int64_t bytes() const { return row.bytes + tile.bytes; }
+};
+
+ChunkPart chunk_part(int64_t total_q, int64_t B, int64_t G, int Hkv, int D, int rows, int slots, int min_tiles) {
+  ChunkPart c;
+  c.rows = rows;
+  c.slots = slots;
+  c.min_tiles = min_tiles;
+  c.max_units = Hkv * (total_q * G / rows + B);
+  c.max_segs = c.max_units + slots;
+  c.bytes = (c.max_segs * rows * (static_cast<int64_t>(D) * 4 + 8) + 255) / 256 * 256;
+  return c;
+}
 
 ChunkSplit chunk_split(int64_t total_q, int64_t B, int64_t max_q, int H, int Hkv, int D) {
   ChunkSplit c;
   const int64_t G = H / Hkv;
   if (max_q <= 0 || max_q > total_q) max_q = total_q;
-  c.row_tiles = max_q * G <= 16 ? 1 : 2;
-  const int64_t R = 16 * c.row_tiles;
-  c.max_units = Hkv * (total_q * G / R + B);
-  c.slots = 8 * sm_count();
-  c.min_tiles = 4;
-  c.max_segs = c.max_units + c.slots;
-  c.bytes = c.max_segs * R * (static_cast<int64_t>(D) * 4 + 8);
+  if (max_q * G > kRowKernelRows) c.tile = chunk_part(total_q, B, G, Hkv, D, kChunkTileRows, sm_count(), 8);
+  // every sequence has more than kRowKernelRows rows only if there is one alone
+  if (max_q * G <= kRowKernelRows || B > 1)
+    c.row = chunk_part(total_q, B, G, Hkv, D, max_q * G <= 16 ? 16 : 32, 8 * sm_count(), 4);
   return c;
+}
+
+uint32_t* chunk_err_word() {
+  void* p = nullptr;
+  if (cudaGetSymbolAddress(&p, g_chunk_err) != cudaSuccess) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  return static_cast<uint32_t*>(p);
 }
 
 }  // namespace
@@ -1561,7 +1606,7 @@ BFA_API int64_t bfa_fwd_chunk_workspace(int64_t total_q, int B, int max_q, int H
     fail(BFA_ERR_INVALID_ARG, "total_q must not be negative and B must be positive");
     return -1;
   }
-  return chunk_split(total_q, B, max_q, H, Hkv, D).bytes;
+  return chunk_split(total_q, B, max_q, H, Hkv, D).bytes();
 }
 
 BFA_API bfa_status bfa_fwd_chunk(const void* q, const int64_t qs[3], const void* k_cache, const void* v_cache,
@@ -1582,12 +1627,14 @@ BFA_API bfa_status bfa_fwd_chunk(const void* q, const int64_t qs[3], const void*
       (s = need_here(lse, "lse", true)) || (s = need_here(slopes, "slopes", true)))
     return s;
   const int G = H / Hkv;
-  const ChunkSplit c = chunk_split(total_q, B, max_q, H, Hkv, D);
-  if (total_q * G >= (int64_t(1) << 30) || c.max_segs >= (int64_t(1) << 31))
+  if (total_q * G >= (int64_t(1) << 30))
     return fail(BFA_ERR_CAPACITY, "%lld query rows are too many for one call", (long long)(total_q * H));
-  if (workspace_bytes < c.bytes)
+  const ChunkSplit c = chunk_split(total_q, B, max_q, H, Hkv, D);
+  if (std::max(c.row.max_segs, c.tile.max_segs) >= (int64_t(1) << 31))
+    return fail(BFA_ERR_CAPACITY, "%lld query rows are too many for one call", (long long)(total_q * H));
+  if (workspace_bytes < c.bytes())
     return fail(BFA_ERR_CAPACITY, "workspace of %lld bytes, %lld needed (bfa_fwd_chunk_workspace)",
-                (long long)workspace_bytes, (long long)c.bytes);
+                (long long)workspace_bytes, (long long)c.bytes());
   if ((s = need_here(workspace, "workspace"))) return s;
   if (reinterpret_cast<uintptr_t>(workspace) & 15u)
     return fail(BFA_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
@@ -1621,18 +1668,52 @@ BFA_API bfa_status bfa_fwd_chunk(const void* q, const int64_t qs[3], const void*
   const float sc = (scale > 0.f) ? scale : 1.0f / std::sqrt(static_cast<float>(D));
   p.scale_log2 = sc * kLog2e;
   p.score = score_params(sc, softcap, slopes);
-  p.rows_lo = 0;
-  p.rows_hi = INT64_MAX;
-  p.slots = c.slots;
-  p.min_tiles = c.min_tiles;
-  p.max_segs = static_cast<int32_t>(c.max_segs);
-  p.max_units = static_cast<int32_t>(c.max_units);
-  const int64_t R = 16 * c.row_tiles;
-  p.ws_o = static_cast<float*>(workspace);
-  p.ws_ml = reinterpret_cast<float2*>(p.ws_o + c.max_segs * R * D);
-  cudaError_t e = launch_chunk_rows(p, c.row_tiles, static_cast<cudaStream_t>(stream));
-  if (e != cudaSuccess) return cuda_fail(e, "chunk kernel");
+  p.wait_ns = g_wait_ns;
+  const cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  auto use = [&](const ChunkPart& part, int64_t rows_lo, int64_t rows_hi) {
+    p.rows_lo = rows_lo;
+    p.rows_hi = rows_hi;
+    p.slots = part.slots;
+    p.min_tiles = part.min_tiles;
+    p.max_segs = static_cast<int32_t>(part.max_segs);
+    p.max_units = static_cast<int32_t>(part.max_units);
+    p.ws_o = reinterpret_cast<float*>(ws);
+    p.ws_ml = reinterpret_cast<float2*>(p.ws_o + part.max_segs * part.rows * D);
+    ws += part.bytes;
+  };
+  if (c.tile.rows) {
+    p.err = chunk_err_word();
+    if (!p.err) return fail(BFA_ERR_CUDA, "the chunk kernels' status word has no address");
+    std::string why;
+    CUtensorMap tk, tv;
+    const int rows = std::min(page_size, static_cast<int>(kTile));
+    if (!make_tmap(&tk, k_cache, D, Hkv, num_pages * page_size, 1, cs[2], cs[1], 0, &why, rows) ||
+        !make_tmap(&tv, v_cache, D, Hkv, num_pages * page_size, 1, cs[2], cs[1], 0, &why, rows))
+      return fail(BFA_ERR_INVALID_ARG, "%s", why.c_str());
+    use(c.tile, c.row.rows ? kRowKernelRows : 0, INT64_MAX);
+    cudaError_t e = launch_chunk_tiles(tk, tv, p, st);
+    if (e != cudaSuccess) return cuda_fail(e, "chunk tile kernel");
+  }
+  if (c.row.rows) {
+    use(c.row, 0, c.tile.rows ? kRowKernelRows : INT64_MAX);
+    cudaError_t e = launch_chunk_rows(p, c.row.rows / 16, st);
+    if (e != cudaSuccess) return cuda_fail(e, "chunk row kernel");
+  }
   return BFA_OK;
+}
+
+BFA_API bfa_status bfa_chunk_device_status(void* stream) {
+  uint32_t* word = chunk_err_word();
+  if (!word) return fail(BFA_ERR_CUDA, "the chunk kernels' status word has no address");
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  uint32_t v = 0;
+  auto cleanup = []() {};
+  BFA_CUDA(cudaMemcpyAsync(&v, word, sizeof(v), cudaMemcpyDeviceToHost, st), "read the chunk status");
+  BFA_CUDA(cudaStreamSynchronize(st), "chunk status");
+  if (!v) return BFA_OK;
+  BFA_CUDA(cudaMemsetAsync(word, 0, sizeof(v), st), "clear the chunk status");
+  return fail(BFA_ERR_TIMEOUT, "a chunk kernel gave up on a wait");
 }
 
 namespace {

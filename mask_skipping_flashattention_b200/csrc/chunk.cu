@@ -19,6 +19,7 @@
 #include "chunk_params.cuh"
 #include "chunk_split.cuh"
 #include "device_once.cuh"
+#include "plan_types.cuh"
 #include "ptx.cuh"
 #include "score.cuh"
 
@@ -326,7 +327,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) k_chunk_rows(const ChunkParams
 }
 
 // Join the pieces of a unit: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,
-// always in the order of the pieces.
+// always in the order of the pieces.  A block takes 16 rows (blockIdx.y) of one unit.
 template <int D, int R, int T>
 __global__ void __launch_bounds__(128) k_chunk_join(const ChunkParams p) {
   __shared__ Piece pc_s;
@@ -336,8 +337,8 @@ __global__ void __launch_bounds__(128) k_chunk_join(const ChunkParams p) {
   if (pc.nseg == 1) return;  // written by its only piece
   const int rows = pc.sp.q_len * p.G, row0 = pc.rt * R;
   constexpr int kCols = D / 4;
-  for (int e = threadIdx.x; e < R * kCols; e += 128) {
-    const int r = e / kCols, c4 = (e % kCols) * 4;
+  for (int e = threadIdx.x; e < 16 * kCols; e += 128) {
+    const int r = blockIdx.y * 16 + e / kCols, c4 = (e % kCols) * 4;
     if (row0 + r >= rows) break;
     float M = -INFINITY;
     for (int i = 0; i < pc.nseg; ++i) {
@@ -369,6 +370,24 @@ __global__ void __launch_bounds__(128) k_chunk_join(const ChunkParams p) {
 // ----------------------------------------------------------------------------
 // launchers (host)
 // ----------------------------------------------------------------------------
+cudaError_t launch_chunk_join(const ChunkParams& p, int rows, int keys, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(p.max_units), static_cast<unsigned>(rows / 16));
+  const bool wide = p.D == 128;
+  if (rows == 16 && keys == kRowKeys) {
+    if (wide) k_chunk_join<128, 16, kRowKeys><<<grid, 128, 0, s>>>(p);
+    else k_chunk_join<64, 16, kRowKeys><<<grid, 128, 0, s>>>(p);
+  } else if (rows == 32 && keys == kRowKeys) {
+    if (wide) k_chunk_join<128, 32, kRowKeys><<<grid, 128, 0, s>>>(p);
+    else k_chunk_join<64, 32, kRowKeys><<<grid, 128, 0, s>>>(p);
+  } else if (rows == kChunkTileRows && keys == kTile) {
+    if (wide) k_chunk_join<128, kChunkTileRows, kTile><<<grid, 128, 0, s>>>(p);
+    else k_chunk_join<64, kChunkTileRows, kTile><<<grid, 128, 0, s>>>(p);
+  } else {
+    return cudaErrorInvalidValue;
+  }
+  return cudaGetLastError();
+}
+
 template <int D, int MT, bool kScore>
 static cudaError_t launch_rows_one(const ChunkParams& p, cudaStream_t s) {
   using C = RowCfg<D, MT>;
@@ -380,8 +399,7 @@ static cudaError_t launch_rows_one(const ChunkParams& p, cudaStream_t s) {
   k_chunk_rows<D, MT, kScore><<<p.max_segs, kRowThreads, C::kSmem, s>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  k_chunk_join<D, C::kRows, kRowKeys><<<p.max_units, 128, 0, s>>>(p);
-  return cudaGetLastError();
+  return launch_chunk_join(p, C::kRows, kRowKeys, s);
 }
 
 template <int D, int MT>

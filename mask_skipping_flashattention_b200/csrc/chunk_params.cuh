@@ -43,6 +43,13 @@ struct ChunkParams {
   uint32_t* err;
 };
 
+// few rows a kv head: 16 or 32 rows a unit (row_tiles 1, 2); with the join
 cudaError_t launch_chunk_rows(const ChunkParams& p, int row_tiles, cudaStream_t s);
+// many rows: 256 rows a unit; with the join
+cudaError_t launch_chunk_tiles(const CUtensorMap& tk, const CUtensorMap& tv, const ChunkParams& p, cudaStream_t s);
+// joins the pieces of units of `rows` rows and key tiles of `keys`
+cudaError_t launch_chunk_join(const ChunkParams& p, int rows, int keys, cudaStream_t s);
+
+constexpr int kChunkTileRows = 256;  // rows of a unit of launch_chunk_tiles
 
 }  // namespace bfa

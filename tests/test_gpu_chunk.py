@@ -271,3 +271,21 @@ def test_empty_calls():
     b.call(out=out, max_q=1)
     torch.cuda.synchronize()
     assert (out == 2).all()
+
+
+def test_a_short_wait_bound_is_reported_and_leaves_nothing_behind():
+    b = Batch([300, 1], [5000, 3000], 8, 2, 128, 64)
+    want = b.call()
+    torch.cuda.synchronize()
+    bfa.chunk_device_status()
+    bfa.set_wait_timeout_ns(1000)  # the first wait for scores outlasts it
+    try:
+        b.call()
+        with pytest.raises(bfa.BfaError) as e:
+            bfa.chunk_device_status()
+        assert e.value.status == "BFA_ERR_TIMEOUT"
+    finally:
+        bfa.set_wait_timeout_ns(0)
+    got = b.call()
+    bfa.chunk_device_status()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
