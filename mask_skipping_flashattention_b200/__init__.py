@@ -53,23 +53,15 @@ def _stream(stream=None):
     return ctypes.c_void_p(int(stream))
 
 
-def _device_of(t):
-    """The device of ``t`` as the current one (CPU tensors are left to the library's refusal)."""
-    return torch.cuda.device(t.device) if t.is_cuda else contextlib.nullcontext()
-
-
 @contextlib.contextmanager
 def _launch_on(t, stream):
     """The device of ``t`` and ``stream`` as the current ones, so that what is allocated inside
     belongs to the stream that uses it; yields (stream handle, finish).  ``finish`` hands such
     results back to the stream that was current."""
-    if not t.is_cuda:
-        yield _stream(stream), lambda *results: None
-        return
     with torch.cuda.device(t.device):
         ambient = torch.cuda.current_stream()
         if stream is None:
-            yield _stream(), lambda *results: None
+            yield ambient.cuda_stream, _keep
             return
         if not isinstance(stream, torch.cuda.Stream):
             stream = torch.cuda.ExternalStream(int(stream), t.device) if int(stream) else torch.cuda.default_stream()
@@ -82,13 +74,44 @@ def _launch_on(t, stream):
                     r.record_stream(ambient)
 
         with torch.cuda.stream(stream):
-            yield _stream(stream), finish
+            yield stream.cuda_stream, finish
+
+
+def _keep(*results):
+    pass
+
+
+def _run_on(t, stream, body):
+    """body(stream handle, finish) with the device of ``t`` and ``stream`` current (see
+    ``_launch_on``), without a context change where they already are: that costs more than
+    a small launch.  CPU tensors are left to the library's refusal."""
+    if not t.is_cuda:
+        return body(0 if stream is None else _stream(stream), _keep)
+    index = t.get_device()
+    if stream is None and index == torch.cuda.current_device():
+        return body(torch._C._cuda_getCurrentRawStream(index), _keep)
+    with _launch_on(t, stream) as (st, finish):
+        return body(st, finish)
 
 
 def _same_device(first, *others):
+    want = first.get_device()  # -1: CPU
     for t in others:
-        if t is not None and t.device != first.device:
+        if t is not None and t.get_device() != want:
             raise ValueError(f"tensors on {first.device} and {t.device}")
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+_Strides3 = ctypes.c_int64 * 3
+
+
+def _strides_of(t):
+    """{batch, token, head} strides of a (B, S, H, D) or packed (T, H, D) tensor."""
+    st = t.stride()
+    return _Strides3(st[0], st[1], st[2]) if len(st) == 4 else _Strides3(0, st[0], st[1])
 
 
 def _score_shape(softcap, slopes, q, H):
@@ -458,7 +481,7 @@ def _result(t, like_shape, dtype, device, name):
     """A caller's result tensor, checked, or a new one."""
     if t is None:
         return torch.empty(like_shape, dtype=dtype, device=device)
-    if tuple(t.shape) != tuple(like_shape) or t.dtype != dtype or t.device != device:
+    if t.shape != like_shape or t.dtype != dtype or t.device != device:
         raise ValueError(f"{name} must be {tuple(like_shape)} {dtype} on {device}")
     if t.dim() and t.stride(-1) != 1:
         raise ValueError(f"the last dim of {name} must be contiguous")
@@ -471,39 +494,43 @@ def _fwd_shaped(plan, q, k, v, scale, out, return_lse, lse, stream, softcap, slo
     cap, slopes = _score_shape(softcap, slopes, q, H)
     if lse is not None and return_lse and not lse.is_contiguous():
         raise ValueError("lse must be contiguous")
-    with _launch_on(q, stream) as (st, finish):
-        own_out, own_lse = out is None, lse is None
-        out = _result(out, q.shape, torch.bfloat16, q.device, "out")
-        lse = _result(lse, lse_shape, torch.float32, q.device, "lse") if return_lse else None
-        _lib.check(_L.bfa_fwd_shaped(plan.handle, _ptr(q), _ptr(k), _ptr(v), _strides3(q), _strides3(k), _strides3(v),
-                                     B, H, Hkv, D, ctypes.c_float(float(scale) if scale is not None else 0.0),
-                                     ctypes.c_float(cap), _ptr(slopes), _ptr(out), _strides3(out), _ptr(lse), st))
-        finish(out if own_out else None, lse if own_lse else None)
-    return out, lse
+
+    def body(st, finish):
+        o = _result(out, q.shape, torch.bfloat16, q.device, "out")
+        l = _result(lse, lse_shape, torch.float32, q.device, "lse") if return_lse else None
+        _lib.check(_L.bfa_fwd_shaped(plan.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), _strides_of(q),
+                                     _strides_of(k), _strides_of(v), B, H, Hkv, D, scale or 0.0, cap, _addr(slopes),
+                                     o.data_ptr(), _strides_of(o), _addr(l), st))
+        finish(o if out is None else None, l if lse is None else None)
+        return o, l
+
+    return _run_on(q, stream, body)
 
 
 def _bwd_shaped(plan, q, k, v, out, dout, lse, scale, dq, dk, dv, stream, softcap, slopes):
     B, H, Hkv, D, lse_shape = _shapes(plan, q, k, v)
-    _same_device(q, k, v, out, dout, lse)
     for t in (out, dout):
         if t.dtype != torch.bfloat16 or t.shape != q.shape or t.stride(-1) != 1:
             raise ValueError("out and dout must be bfloat16 with the shape of q and a contiguous head dim")
-    if lse is None or lse.dtype != torch.float32 or tuple(lse.shape) != tuple(lse_shape):
+    if lse is None or lse.dtype != torch.float32 or lse.shape != lse_shape:
         raise ValueError(f"lse (float32 {tuple(lse_shape)}, from fwd) is required")
+    _same_device(q, k, v, out, dout, lse)
     cap, slopes = _score_shape(softcap, slopes, q, H)
-    with _launch_on(q, stream) as (st, finish):
-        own = [g is None for g in (dq, dk, dv)]
-        dq = _result(dq, q.shape, torch.bfloat16, q.device, "dq")
-        dk = _result(dk, k.shape, torch.bfloat16, q.device, "dk")
-        dv = _result(dv, v.shape, torch.bfloat16, q.device, "dv")
-        lse = lse.contiguous()
-        _lib.check(_L.bfa_bwd_shaped(plan.handle, _ptr(q), _ptr(k), _ptr(v), _ptr(out), _ptr(dout), _ptr(lse),
-                                     _strides3(q), _strides3(k), _strides3(v), _strides3(out), _strides3(dout), B, H,
-                                     Hkv, D, ctypes.c_float(float(scale) if scale is not None else 0.0),
-                                     ctypes.c_float(cap), _ptr(slopes), _ptr(dq), _ptr(dk), _ptr(dv), _strides3(dq),
-                                     _strides3(dk), _strides3(dv), st))
-        finish(*(g for g, mine in zip((dq, dk, dv), own) if mine))
-    return dq, dk, dv
+
+    def body(st, finish):
+        gq = _result(dq, q.shape, torch.bfloat16, q.device, "dq")
+        gk = _result(dk, k.shape, torch.bfloat16, q.device, "dk")
+        gv = _result(dv, v.shape, torch.bfloat16, q.device, "dv")
+        l = lse.contiguous()
+        _lib.check(_L.bfa_bwd_shaped(plan.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                                     dout.data_ptr(), l.data_ptr(), _strides_of(q), _strides_of(k), _strides_of(v),
+                                     _strides_of(out), _strides_of(dout), B, H, Hkv, D, scale or 0.0, cap,
+                                     _addr(slopes), gq.data_ptr(), gk.data_ptr(), gv.data_ptr(), _strides_of(gq),
+                                     _strides_of(gk), _strides_of(gv), st))
+        finish(gq if dq is None else None, gk if dk is None else None, gv if dv is None else None)
+        return gq, gk, gv
+
+    return _run_on(q, stream, body)
 
 
 def bwd(plan, q, k, v, out, dout, lse, scale=None, dq=None, dk=None, dv=None, stream=None, softcap=None, slopes=None):
@@ -596,7 +623,7 @@ def _check_cache(k_cache, v_cache, block_table, cu_seqlens, seqused_k):
     for t, name in ((block_table, "block_table"), (cu_seqlens, "cu_seqlens"), (seqused_k, "seqused_k")):
         if t.dtype not in (torch.int32, torch.int64):
             raise TypeError(f"{name} must be int32 or int64")
-        ints.append(t.to(torch.int32).contiguous())
+        ints.append(t if t.dtype is torch.int32 and t.is_contiguous() else t.to(torch.int32).contiguous())
     _same_device(k_cache, v_cache, *ints)
     return ints
 
@@ -612,8 +639,8 @@ def _check_packed(t, name, heads, D):
 
 def _cache_strides(c):
     # a cache of one page has no page stride of its own
-    page = c.stride(0) if c.shape[0] > 1 else c.shape[1] * c.stride(1)
-    return (ctypes.c_int64 * 3)(page, c.stride(1), c.stride(2))
+    st = c.stride()
+    return _Strides3(st[0] if c.shape[0] > 1 else c.shape[1] * st[1], st[1], st[2])
 
 
 def fwd_chunk(q, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, *, max_q=0, scale=None, window_left=-1,
@@ -631,32 +658,33 @@ def fwd_chunk(q, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, *, max_
     and a captured call follows their contents.  Rows of q behind the last sequence
     are left as they are in out and lse.
     """
-    block_table, cu, used = _check_cache(k_cache, v_cache, block_table, cu_seqlens_q, seqused_k)
+    table, cu, used = _check_cache(k_cache, v_cache, block_table, cu_seqlens_q, seqused_k)
     num_pages, page_size, Hkv, D = k_cache.shape
+    max_q, window_left = int(max_q), int(window_left)
     _check_packed(q, "q", None, D)
     _same_device(q, k_cache, workspace)
     T, H, _ = q.shape
     B = used.numel()
     cap, slopes = _score_shape(softcap, slopes, q, H)
-    need = _L.bfa_fwd_chunk_workspace(T, B, int(max_q), H, Hkv, D)
+    need = _L.bfa_fwd_chunk_workspace(T, B, max_q, H, Hkv, D)
     if need < 0:
         _lib.check(-2 if D not in (64, 128) else -1)
     if lse is not None and return_lse and not lse.is_contiguous():
         raise ValueError("lse must be contiguous")
-    with _launch_on(q, stream) as (st, finish):
-        own_out, own_lse = out is None, lse is None
-        out = _result(out, q.shape, torch.bfloat16, q.device, "out")
-        lse = _result(lse, (H, T), torch.float32, q.device, "lse") if return_lse else None
-        if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        _lib.check(_L.bfa_fwd_chunk(_ptr(q), _strides3(q), _ptr(k_cache), _ptr(v_cache), _cache_strides(k_cache),
-                                    num_pages, page_size, _ptr(block_table), block_table.shape[1], _ptr(cu), _ptr(used),
-                                    B, T, int(max_q), H, Hkv, D,
-                                    ctypes.c_float(float(scale) if scale is not None else 0.0), int(window_left),
-                                    ctypes.c_float(cap), _ptr(slopes), _ptr(out), _strides3(out), _ptr(lse),
-                                    _ptr(workspace), workspace.numel() * workspace.element_size(), st))
-        finish(out if own_out else None, lse if own_lse else None)
-    return out, lse
+
+    def body(st, finish):
+        o = _result(out, q.shape, torch.bfloat16, q.device, "out")
+        l = _result(lse, (H, T), torch.float32, q.device, "lse") if return_lse else None
+        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if workspace is None else workspace
+        _lib.check(_L.bfa_fwd_chunk(q.data_ptr(), _strides_of(q), k_cache.data_ptr(), v_cache.data_ptr(),
+                                    _cache_strides(k_cache), num_pages, page_size, table.data_ptr(), table.shape[1],
+                                    cu.data_ptr(), used.data_ptr(), B, T, max_q, H, Hkv, D, scale or 0.0, window_left,
+                                    cap, _addr(slopes), o.data_ptr(), _strides_of(o), _addr(l), ws.data_ptr(),
+                                    ws.numel() * ws.element_size(), st))
+        finish(o if out is None else None, l if lse is None else None)
+        return o, l
+
+    return _run_on(q, stream, body)
 
 
 def chunk_device_status(stream=None):
@@ -723,15 +751,17 @@ def rope(x, positions, inv_freq, *, interleaved=False, amplitude=1.0, inverse=Fa
         raise ValueError("an in-place result must be x itself")
     if x.numel() == 0:
         return out if out is not None else torch.empty_like(x)
-    with _launch_on(x, stream) as (st, finish):
-        own_out = out is None
-        out = _result(out, x.shape, torch.bfloat16, x.device, "out")
-        _lib.check(_L.bfa_rope(_ptr(x), _strides3(x), _ptr(out), _strides3(out), _ptr(positions),
-                               1 if positions.dtype == torch.int64 else 0, S if positions.dim() == 2 else 0,
-                               _ptr(inv_freq), rotary, B, S, H, D, 1 if interleaved else 0,
-                               ctypes.c_float(float(amplitude)), 1 if inverse else 0, st))
-        finish(out if own_out else None)
-    return out
+
+    def body(st, finish):
+        y = _result(out, x.shape, torch.bfloat16, x.device, "out")
+        _lib.check(_L.bfa_rope(x.data_ptr(), _strides_of(x), y.data_ptr(), _strides_of(y), positions.data_ptr(),
+                               1 if positions.dtype is torch.int64 else 0, S if positions.dim() == 2 else 0,
+                               _addr(inv_freq), rotary, B, S, H, D, 1 if interleaved else 0, amplitude,
+                               1 if inverse else 0, st))
+        finish(y if out is None else None)
+        return y
+
+    return _run_on(x, stream, body)
 
 
 def append_paged(k, v, k_cache, v_cache, block_table, cu_seqlens, seqused_k, *, q=None, q_out=None, inv_freq=None,
@@ -744,7 +774,7 @@ def append_paged(k, v, k_cache, v_cache, block_table, cu_seqlens, seqused_k, *, 
     ``inv_freq`` None: keys and queries are copied.  Rows behind the last sequence are left
     out.  Lengths and pages stay on the device, as for ``fwd_chunk``.
     """
-    block_table, cu, used = _check_cache(k_cache, v_cache, block_table, cu_seqlens, seqused_k)
+    table, cu, used = _check_cache(k_cache, v_cache, block_table, cu_seqlens, seqused_k)
     num_pages, page_size, Hkv, D = k_cache.shape
     _check_packed(k, "k", Hkv, D)
     _check_packed(v, "v", Hkv, D)
@@ -762,17 +792,17 @@ def append_paged(k, v, k_cache, v_cache, block_table, cu_seqlens, seqused_k, *, 
     elif q_out is not None:
         raise ValueError("q_out without q")
     rotary, inv_freq = _check_frequencies(inv_freq, k)
-    with _launch_on(k, stream) as (st, finish):
-        own_out = q_out is None
-        if q is not None:
-            q_out = _result(q_out, q.shape, torch.bfloat16, q.device, "q_out")
-        none3 = (ctypes.c_int64 * 3)(0, 0, 0)
-        _lib.check(_L.bfa_append_paged(_ptr(k), _strides3(k), _ptr(v), _strides3(v), _ptr(q),
-                                       none3 if q is None else _strides3(q), _ptr(q_out),
-                                       none3 if q is None else _strides3(q_out), _ptr(k_cache), _ptr(v_cache),
-                                       _cache_strides(k_cache), num_pages, page_size, _ptr(block_table),
-                                       block_table.shape[1], _ptr(cu), _ptr(used), used.numel(), T, H, Hkv, D,
-                                       _ptr(inv_freq), rotary, 1 if interleaved else 0,
-                                       ctypes.c_float(float(amplitude)), st))
-        finish(q_out if own_out else None)
-    return q_out
+
+    def body(st, finish):
+        qo = None if q is None else _result(q_out, q.shape, torch.bfloat16, q.device, "q_out")
+        none3 = _Strides3(0, 0, 0)
+        _lib.check(_L.bfa_append_paged(k.data_ptr(), _strides_of(k), v.data_ptr(), _strides_of(v), _addr(q),
+                                       none3 if q is None else _strides_of(q), _addr(qo),
+                                       none3 if q is None else _strides_of(qo), k_cache.data_ptr(), v_cache.data_ptr(),
+                                       _cache_strides(k_cache), num_pages, page_size, table.data_ptr(), table.shape[1],
+                                       cu.data_ptr(), used.data_ptr(), used.numel(), T, H, Hkv, D, _addr(inv_freq),
+                                       rotary, 1 if interleaved else 0, amplitude, st))
+        finish(qo if q_out is None else None)
+        return qo
+
+    return _run_on(k, stream, body)

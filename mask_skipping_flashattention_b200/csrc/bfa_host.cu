@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -1491,16 +1492,20 @@ static __device__ uint32_t g_chunk_err;
 
 namespace {
 
-// device memory of the current device, 16-byte aligned
+// device memory of the current device
 bfa_status need_here(const void* p, const char* name, bool allow_null = false) {
-  bfa_status s = need_device(p, name, allow_null);
-  if (s != BFA_OK || !p) return s;
+  if (p == nullptr) return allow_null ? BFA_OK : fail(BFA_ERR_INVALID_ARG, "%s is NULL", name);
   cudaPointerAttributes a;
-  int dev = 0;
-  if (cudaPointerGetAttributes(&a, p) != cudaSuccess || cudaGetDevice(&dev) != cudaSuccess) {
+  cudaError_t e = cudaPointerGetAttributes(&a, p);
+  if (e != cudaSuccess) {
     cudaGetLastError();
-    return fail(BFA_ERR_NOT_DEVICE, "%s is not a device pointer", name);
+    return fail(BFA_ERR_NOT_DEVICE, "%s is not a device pointer (%s)", name, cudaGetErrorString(e));
   }
+  if (a.type != cudaMemoryTypeDevice && a.type != cudaMemoryTypeManaged)
+    return fail(BFA_ERR_NOT_DEVICE, "%s is not device memory (CPU tensors are not supported)", name);
+  int dev = 0;
+  e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return cuda_fail(e, "current device");
   if (a.type == cudaMemoryTypeDevice && a.device != dev)
     return fail(BFA_ERR_INVALID_ARG, "%s is on device %d, the current device is %d", name, a.device, dev);
   return BFA_OK;
@@ -1552,50 +1557,67 @@ bfa_status check_cache(const void* k_cache, const void* v_cache, const int64_t* 
   return BFA_OK;
 }
 
-// The split of a chunk call.  Sequences with up to kRowKernelRows query rows a kv
-// head go to the row kernel, longer ones to the tile kernel; a call whose max_q
-// rules one of them out launches only the other, which then serves every sequence.
-constexpr int64_t kRowKernelRows = 64;
-
+// The kernels of a chunk call.  Sequences with up to 16 query rows a kv head (one
+// unit of the row kernel) go to the row kernel, longer ones to the tile kernel: at
+// 16 rows the row kernel takes 58 us against 63 on 8 sequences of 4096 keys (8 kv
+// heads, D 128), at 32 rows 88 against 67.  A call whose max_q rules one of them
+// out launches only the other, which then serves every sequence.
 struct ChunkPart {
   int rows = 0;  // rows of a unit (0: not launched)
-  int slots = 0, min_tiles = 0;
-  int64_t max_units = 0, max_segs = 0, bytes = 0;
+  int slots = 0, min_share = 0, start_cost = 0;
+  int64_t bytes = 0;
 };
 struct ChunkSplit {
   ChunkPart row, tile;
   int64_t bytes() const { return row.bytes + tile.bytes; }
 };
 
-ChunkPart chunk_part(int64_t total_q, int64_t B, int64_t G, int Hkv, int D, int rows, int slots, int min_tiles) {
-  ChunkPart c;
-  c.rows = rows;
-  c.slots = slots;
-  c.min_tiles = min_tiles;
-  c.max_units = Hkv * (total_q * G / rows + B);
-  c.max_segs = c.max_units + slots;
-  c.bytes = (c.max_segs * rows * (static_cast<int64_t>(D) * 4 + 8) + 255) / 256 * 256;
-  return c;
+// the places of a launch's cut units, two a block, and its notes of the cuts
+int64_t part_bytes(int slots, int rows, int D) {
+  return (static_cast<int64_t>(2 * slots) * rows * (static_cast<int64_t>(D) * 4 + 8) + slots * kChunkCutBytes + 255) /
+         256 * 256;
 }
 
 ChunkSplit chunk_split(int64_t total_q, int64_t B, int64_t max_q, int H, int Hkv, int D) {
   ChunkSplit c;
   const int64_t G = H / Hkv;
   if (max_q <= 0 || max_q > total_q) max_q = total_q;
-  if (max_q * G > kRowKernelRows) c.tile = chunk_part(total_q, B, G, Hkv, D, kChunkTileRows, sm_count(), 8);
-  // every sequence has more than kRowKernelRows rows only if there is one alone
-  if (max_q * G <= kRowKernelRows || B > 1)
-    c.row = chunk_part(total_q, B, G, Hkv, D, max_q * G <= 16 ? 16 : 32, 8 * sm_count(), 4);
+  const bool few = max_q * G <= kChunkRows;
+  if (!few) {
+    c.tile.rows = kChunkTileRows;
+    c.tile.slots = sm_count();
+    c.tile.min_share = 4;
+    c.tile.start_cost = 2;
+    c.tile.bytes = part_bytes(c.tile.slots, c.tile.rows, D);
+  }
+  if (few || (B > 1 && G <= kChunkRows)) {  // one sequence alone goes to the tile kernel whatever its length
+    c.row.rows = kChunkRows;
+    c.row.slots = 2 * sm_count();
+    c.row.min_share = 4;
+    c.row.start_cost = 2;
+    c.row.bytes = part_bytes(c.row.slots, c.row.rows, D);
+  }
   return c;
 }
 
+// its address, looked up once a device
 uint32_t* chunk_err_word() {
+  static std::atomic<uint32_t*> known[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  uint32_t* w = known[dev].load(std::memory_order_acquire);
+  if (w) return w;
   void* p = nullptr;
   if (cudaGetSymbolAddress(&p, g_chunk_err) != cudaSuccess) {
     cudaGetLastError();
     return nullptr;
   }
-  return static_cast<uint32_t*>(p);
+  w = static_cast<uint32_t*>(p);
+  known[dev].store(w, std::memory_order_release);
+  return w;
 }
 
 }  // namespace
@@ -1627,11 +1649,9 @@ BFA_API bfa_status bfa_fwd_chunk(const void* q, const int64_t qs[3], const void*
       (s = need_here(lse, "lse", true)) || (s = need_here(slopes, "slopes", true)))
     return s;
   const int G = H / Hkv;
-  if (total_q * G >= (int64_t(1) << 30))
-    return fail(BFA_ERR_CAPACITY, "%lld query rows are too many for one call", (long long)(total_q * H));
+  if (total_q * G >= (int64_t(1) << 23))
+    return fail(BFA_ERR_CAPACITY, "%lld new tokens of %d heads a kv head are too many for one call", (long long)total_q, G);
   const ChunkSplit c = chunk_split(total_q, B, max_q, H, Hkv, D);
-  if (std::max(c.row.max_segs, c.tile.max_segs) >= (int64_t(1) << 31))
-    return fail(BFA_ERR_CAPACITY, "%lld query rows are too many for one call", (long long)(total_q * H));
   if (workspace_bytes < c.bytes())
     return fail(BFA_ERR_CAPACITY, "workspace of %lld bytes, %lld needed (bfa_fwd_chunk_workspace)",
                 (long long)workspace_bytes, (long long)c.bytes());
@@ -1669,37 +1689,43 @@ BFA_API bfa_status bfa_fwd_chunk(const void* q, const int64_t qs[3], const void*
   p.scale_log2 = sc * kLog2e;
   p.score = score_params(sc, softcap, slopes);
   p.wait_ns = g_wait_ns;
+  p.err = chunk_err_word();
+  if (!p.err) return fail(BFA_ERR_CUDA, "the chunk kernels' status word has no address");
   const cudaStream_t st = static_cast<cudaStream_t>(stream);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
-  auto use = [&](const ChunkPart& part, int64_t rows_lo, int64_t rows_hi) {
-    p.rows_lo = rows_lo;
-    p.rows_hi = rows_hi;
-    p.slots = part.slots;
-    p.min_tiles = part.min_tiles;
-    p.max_segs = static_cast<int32_t>(part.max_segs);
-    p.max_units = static_cast<int32_t>(part.max_units);
-    p.ws_o = reinterpret_cast<float*>(ws);
-    p.ws_ml = reinterpret_cast<float2*>(p.ws_o + part.max_segs * part.rows * D);
+  auto part_params = [&](const ChunkPart& part, int32_t rows_lo, int32_t rows_hi) {
+    ChunkParams x = p;
+    x.rows_lo = rows_lo;
+    x.rows_hi = rows_hi;
+    x.slots = part.slots;
+    x.min_share = part.min_share;
+    x.start_cost = part.start_cost;
+    x.ws_o = reinterpret_cast<float*>(ws);
+    x.ws_ml = reinterpret_cast<float2*>(x.ws_o + static_cast<int64_t>(2 * part.slots) * part.rows * D);
+    x.ws_cuts = x.ws_ml + static_cast<int64_t>(2 * part.slots) * part.rows;
     ws += part.bytes;
+    return x;
   };
+  const bool both = c.row.rows && c.tile.rows;
+  const ChunkParams tile = part_params(c.tile, both ? kChunkRows : 0, INT32_MAX);
+  const ChunkParams row = part_params(c.row, 0, both ? kChunkRows : INT32_MAX);
+  cudaError_t e;
   if (c.tile.rows) {
-    p.err = chunk_err_word();
-    if (!p.err) return fail(BFA_ERR_CUDA, "the chunk kernels' status word has no address");
     std::string why;
     CUtensorMap tk, tv;
     const int rows = std::min(page_size, static_cast<int>(kTile));
     if (!make_tmap(&tk, k_cache, D, Hkv, num_pages * page_size, 1, cs[2], cs[1], 0, &why, rows) ||
         !make_tmap(&tv, v_cache, D, Hkv, num_pages * page_size, 1, cs[2], cs[1], 0, &why, rows))
       return fail(BFA_ERR_INVALID_ARG, "%s", why.c_str());
-    use(c.tile, c.row.rows ? kRowKernelRows : 0, INT64_MAX);
-    cudaError_t e = launch_chunk_tiles(tk, tv, p, st);
+    e = launch_chunk_tiles(tk, tv, tile, st);
     if (e != cudaSuccess) return cuda_fail(e, "chunk tile kernel");
   }
   if (c.row.rows) {
-    use(c.row, 0, c.tile.rows ? kRowKernelRows : INT64_MAX);
-    cudaError_t e = launch_chunk_rows(p, c.row.rows / 16, st);
+    e = launch_chunk_rows(row, both, st);
     if (e != cudaSuccess) return cuda_fail(e, "chunk row kernel");
   }
+  e = launch_chunk_join(row, tile, st);
+  if (e != cudaSuccess) return cuda_fail(e, "chunk join kernel");
   return BFA_OK;
 }
 

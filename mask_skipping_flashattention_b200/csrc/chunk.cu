@@ -72,346 +72,433 @@ __device__ __forceinline__ void store4(const ChunkParams& p, int64_t tok, int h,
   *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
 
-template <int D, int MT>
+template <int D>
 struct RowCfg {
-  static constexpr int kRows = 16 * MT;
-  static constexpr int kSlice = 16 * D * 2;                        // bytes of 16 keys (or values)
+  static constexpr int kSlice = 16 * D * 2;                          // bytes of 16 keys (or values)
   static constexpr int kRing = kRowWarps * kRowStages * 2 * kSlice;  // also holds the warps' sums at the end
-  static constexpr int kSums = kRowWarps * kRows * D * 4;
+  static constexpr int kSums = kRowWarps * kChunkRows * D * 4;
   static constexpr int kSmem = kRing > kSums ? kRing : kSums;
 };
 
 }  // namespace
 
-template <int D, int MT, bool kScore>
+template <int D, bool kScore>
 __global__ void __launch_bounds__(kRowThreads, 2) k_chunk_rows(const ChunkParams p) {
-  using C = RowCfg<D, MT>;
+  using C = RowCfg<D>;
   extern __shared__ __align__(1024) uint8_t smem_rows[];
   __shared__ Piece pc_s;
-  __shared__ int64_t warp_sums[kRowWarps];
-  __shared__ float2 ml_s[kRowWarps][C::kRows];
-  if (!find_piece<C::kRows, kRowKeys>(p, blockIdx.x, false, &pc_s, warp_sums)) return;
-  const Piece& pc = pc_s;
+  __shared__ int have_s;
+  __shared__ float2 ml_s[kRowWarps][kChunkRows];
+  grid_trigger();  // the join may take the place of blocks that are done
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int q_len = pc.sp.q_len, kv = pc.sp.kv, q0 = pc.sp.q0;
-  const int rows = q_len * p.G;  // served sequences: fits
-  const int row0 = pc.rt * C::kRows;
-  // keys that some row of the tile sees
-  const int tok_a = row0 / p.G, tok_b = min(row0 + C::kRows, rows) - 1;
-  const int pos_a = kv - q_len + tok_a, pos_b = kv - q_len + tok_b / p.G;
-  const int lo_u = p.window >= 0 ? max(0, pos_a - p.window + 1) : 0, hi_u = min(kv, pos_b + 1);
-
-  // this thread's rows: g + 8 i of each 16-row block
-  int pos[MT][2], hi[MT][2], lo[MT][2];
-  float slope[MT][2];
-  uint32_t qf[MT][D / 16][4];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-    const __nv_bfloat16* qr[2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const int r = row0 + mt * 16 + (lane >> 2) + 8 * i;
-      const bool in = r < rows;
-      const int t = in ? r / p.G : 0;
-      const int h = pc.hk * p.G + (in ? r - t * p.G : 0);
-      pos[mt][i] = kv - q_len + t;
-      hi[mt][i] = in ? min(kv, pos[mt][i] + 1) : 0;
-      lo[mt][i] = p.window >= 0 ? max(0, pos[mt][i] - p.window + 1) : 0;
-      slope[mt][i] = (kScore && p.score.slopes) ? __ldg(p.score.slopes + h) * kLog2e : 0.f;
-      qr[i] = in ? p.q + (static_cast<int64_t>(q0) + t) * p.q_ss + static_cast<int64_t>(h) * p.q_sh : nullptr;
+  // warp 0 walks this block's share of the line
+  Walk walk;
+  int64_t left = 0;
+  bool more = false;
+  if (warp == 0) {
+    const Line ln = line_of<kChunkRows, kRowKeys>(p);
+    const int64_t pos = ln.share * blockIdx.x;
+    left = min(ln.share, ln.total - pos);
+    more = left > 0;
+    if (more) walk = walk_to<kChunkRows, kRowKeys>(p, pos);
+    if (lane == 0) note_cut(p, walk, ln.share, blockIdx.x, more);
+  }
+  for (;;) {
+    if (warp == 0) {
+      if (more) {
+        const int64_t x1 = min(walk.w, walk.x + left);
+        const Piece pc = piece_of<kChunkRows, kRowKeys>(p, walk, x1, blockIdx.x);
+        left -= x1 - walk.x;
+        if (lane == 0) pc_s = pc;
+      }
+      if (lane == 0) have_s = more;
+      more = more && left > 0 && walk.template next<kChunkRows, kRowKeys>(p);
     }
+    __syncthreads();
+    if (!have_s) break;
+    const Piece pc = pc_s;
+    const int q_len = pc.sp.q_len, kv = pc.sp.kv, q0 = pc.sp.q0;
+    const int rows = q_len * p.G;  // served sequences: fits
+    const int row0 = pc.rt * kChunkRows;
+    const int lo_u = pc.lo, hi_u = pc.hi;  // keys that some row of the unit sees
+
+    // ring of this warp: stage st holds 16 keys, then their values
+    const uint32_t ring_u = smem_u32(smem_rows + warp * (kRowStages * 2 * C::kSlice));
+    const int n = pc.t1 - pc.t0;
+    const int kb0 = pc.t0 * kRowKeys + warp * 16;  // first key of slice 0
+    const int32_t* bt = p.block_table + static_cast<int64_t>(pc.s) * p.pages_per_seq;
+    constexpr int kChunks = D / 8;      // 16-byte chunks of a row
+    constexpr int kPer = 32 / kChunks;  // rows a copy instruction covers
+    // place in the cache of the lane's key of slice t (lanes 16..31 repeat), -1: none
+    auto place = [&](int t) -> int64_t {
+      const int key = kb0 + t * kRowKeys + (lane & 15);
+      if (t >= n || key < lo_u || key >= hi_u) return -1;
+      const int pi = key / p.page_size;
+      const int64_t page = __ldg(bt + pi);
+      if (page < 0 || page >= p.num_pages) return -1;
+      return page * p.c_sp + static_cast<int64_t>(key - pi * p.page_size) * p.c_st;
+    };
+    auto issue = [&](int64_t at, int st) {
+      const uint32_t dk = ring_u + st * 2 * C::kSlice, dv = dk + C::kSlice;
+      const int64_t head = static_cast<int64_t>(pc.hk) * p.c_sh;
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-      const int c = kk * 16 + (lane & 3) * 2;
+      for (int it = 0; it < 16 / kPer; ++it) {
+        const int row = it * kPer + lane / kChunks, ch = lane % kChunks;
+        const int64_t o = __shfl_sync(0xffffffffu, at, row);
+        const uint32_t d = row * (D * 2) + ((ch ^ (row & 7)) << 4);
+        const int64_t e = (o < 0 ? 0 : o) + head + ch * 8;
+        cp_async16(dk + d, p.k_cache + e, o >= 0);
+        cp_async16(dv + d, p.v_cache + e, o >= 0);
+      }
+    };
+    // the first copies go out before anything else is read
+    int64_t at[kRowStages];
+#pragma unroll
+    for (int t = 0; t < kRowStages; ++t) at[t] = place(t);
+#pragma unroll
+    for (int t = 0; t < kRowStages - 1; ++t) {
+      if (t < n) issue(at[t], t);
+      cp_async_commit();
+    }
+    int64_t at_next = at[kRowStages - 1];
+
+    // this thread's rows: lane / 4 + 8 i
+    int pos[2], hi[2], lo[2];
+    float slope[2];
+    uint32_t qf[D / 16][4];
+    {
+      const __nv_bfloat16* qr[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        qf[mt][kk][i] = qr[i] ? *reinterpret_cast<const uint32_t*>(qr[i] + c) : 0u;
-        qf[mt][kk][2 + i] = qr[i] ? *reinterpret_cast<const uint32_t*>(qr[i] + c + 8) : 0u;
+        const int r = row0 + (lane >> 2) + 8 * i;
+        const bool in = r < rows;
+        const int t = in ? r / p.G : 0;
+        const int h = pc.hk * p.G + (in ? r - t * p.G : 0);
+        pos[i] = kv - q_len + t;
+        hi[i] = in ? min(kv, pos[i] + 1) : 0;
+        lo[i] = p.window >= 0 ? max(0, pos[i] - p.window + 1) : 0;
+        slope[i] = (kScore && p.score.slopes) ? __ldg(p.score.slopes + h) * kLog2e : 0.f;
+        qr[i] = in ? p.q + (static_cast<int64_t>(q0) + t) * p.q_ss + static_cast<int64_t>(h) * p.q_sh : nullptr;
+      }
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const int c = kk * 16 + (lane & 3) * 2;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          qf[kk][i] = qr[i] ? *reinterpret_cast<const uint32_t*>(qr[i] + c) : 0u;
+          qf[kk][2 + i] = qr[i] ? *reinterpret_cast<const uint32_t*>(qr[i] + c + 8) : 0u;
+        }
       }
     }
-  }
 
-  // ring of this warp: stage st holds 16 keys, then their values
-  uint8_t* const ring = smem_rows + warp * (kRowStages * 2 * C::kSlice);
-  const uint32_t ring_u = smem_u32(ring);
-  const int n = pc.t1 - pc.t0;
-  const int kb0 = pc.t0 * kRowKeys + warp * 16;  // first key of slice 0
-  const int32_t* bt = p.block_table + static_cast<int64_t>(pc.s) * p.pages_per_seq;
-  constexpr int kChunks = D / 8;          // 16-byte chunks of a row
-  constexpr int kPer = 32 / kChunks;      // rows a copy instruction covers
-  // place in the cache of the lane's key of slice t (lanes 16..31 repeat), -1: none
-  auto place = [&](int t) -> int64_t {
-    const int key = kb0 + t * kRowKeys + (lane & 15);
-    if (t >= n || key < lo_u || key >= hi_u) return -1;
-    const int pi = key / p.page_size;
-    const int64_t page = __ldg(bt + pi);
-    if (page < 0 || page >= p.num_pages) return -1;
-    return page * p.c_sp + static_cast<int64_t>(key - pi * p.page_size) * p.c_st;
-  };
-  auto issue = [&](int64_t at, int st) {
-    const uint32_t dk = ring_u + st * 2 * C::kSlice, dv = dk + C::kSlice;
-    const int64_t head = static_cast<int64_t>(pc.hk) * p.c_sh;
+    float acc[D / 8][4];
+    float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
-    for (int it = 0; it < 16 / kPer; ++it) {
-      const int row = it * kPer + lane / kChunks, ch = lane % kChunks;
-      const int64_t o = __shfl_sync(0xffffffffu, at, row);
-      const uint32_t d = row * (D * 2) + ((ch ^ (row & 7)) << 4);
-      const int64_t e = (o < 0 ? 0 : o) + head + ch * 8;
-      cp_async16(dk + d, p.k_cache + e, o >= 0);
-      cp_async16(dv + d, p.v_cache + e, o >= 0);
-    }
-  };
+    for (int d = 0; d < D / 8; ++d) acc[d][0] = acc[d][1] = acc[d][2] = acc[d][3] = 0.f;
 
-  float acc[MT][D / 8][4];
-  float m[MT][2], l[MT][2];
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
-#pragma unroll
-    for (int d = 0; d < D / 8; ++d) acc[mt][d][0] = acc[mt][d][1] = acc[mt][d][2] = acc[mt][d][3] = 0.f;
-    m[mt][0] = m[mt][1] = -INFINITY;
-    l[mt][0] = l[mt][1] = 0.f;
-  }
-#pragma unroll
-  for (int t = 0; t < kRowStages - 1; ++t) {
-    if (t < n) issue(place(t), t);
-    cp_async_commit();
-  }
-  int64_t at_next = place(kRowStages - 1);
-
-  int st = 0;
-  for (int t = 0; t < n; ++t) {
-    cp_async_wait<kRowStages - 2>();
-    __syncwarp();
-    {  // refill the stage that the previous slice left
-      const int tn = t + kRowStages - 1;
-      const int sn = st == 0 ? kRowStages - 1 : st - 1;
-      if (tn < n) issue(at_next, sn);
-      cp_async_commit();
-      at_next = place(tn + 1);
-    }
-    const uint32_t sk = ring_u + st * 2 * C::kSlice, sv = sk + C::kSlice;
-    st = st + 1 == kRowStages ? 0 : st + 1;
-    const int kb = kb0 + t * kRowKeys;
-    if (kb >= hi_u || kb + 16 <= lo_u) continue;  // no row sees any of these keys
-
-    // S = Q K^T: 16 keys in two blocks of 8
-    float s[MT][2][4];
-#pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) s[mt][j][0] = s[mt][j][1] = s[mt][j][2] = s[mt][j][3] = 0.f;
-#pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk) {
-      const int key = ((lane >> 4) << 3) + (lane & 7), ch = kk * 2 + ((lane >> 3) & 1);
-      uint32_t b[4];
-      ldsm4(sk + key * (D * 2) + ((ch ^ (key & 7)) << 4), b);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        mma16816(s[mt][0], qf[mt][kk], b[0], b[1]);
-        mma16816(s[mt][1], qf[mt][kk], b[2], b[3]);
+    int st = 0;
+    for (int t = 0; t < n; ++t) {
+      cp_async_wait<kRowStages - 2>();
+      __syncwarp();
+      {  // refill the stage that the previous slice left
+        const int tn = t + kRowStages - 1;
+        const int sn = st == 0 ? kRowStages - 1 : st - 1;
+        if (tn < n) issue(at_next, sn);
+        cp_async_commit();
+        at_next = place(tn + 1);
       }
-    }
-    uint32_t pf[MT][4];
+      const uint32_t sk = ring_u + st * 2 * C::kSlice, sv = sk + C::kSlice;
+      st = st + 1 == kRowStages ? 0 : st + 1;
+      const int kb = kb0 + t * kRowKeys;
+      if (kb >= hi_u || kb + 16 <= lo_u) continue;  // no row sees any of these keys
+
+      // S = Q K^T: 16 keys in two blocks of 8
+      float s[2][4];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
+      for (int j = 0; j < 2; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.f;
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const int key = ((lane >> 4) << 3) + (lane & 7), ch = kk * 2 + ((lane >> 3) & 1);
+        uint32_t b[4];
+        ldsm4(sk + key * (D * 2) + ((ch ^ (key & 7)) << 4), b);
+        mma16816(s[0], qf[kk], b[0], b[1]);
+        mma16816(s[1], qf[kk], b[2], b[3]);
+      }
       // shaped scores in log2 units; masked ones -inf
 #pragma unroll
       for (int j = 0; j < 2; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const int i = e >> 1, key = kb + j * 8 + (lane & 3) * 2 + (e & 1);
-          float z = s[mt][j][e];
+          float z = s[j][e];
           if constexpr (kScore) {
             z = p.score.c1 != 0.f ? p.score.c1 * tanh_any(z * p.score.c0) : z * p.scale_log2;
-            z = fmaf(-slope[mt][i], static_cast<float>(pos[mt][i] - key), z);
+            z = fmaf(-slope[i], static_cast<float>(pos[i] - key), z);
           } else {
             z *= p.scale_log2;
           }
-          s[mt][j][e] = (key >= lo[mt][i] && key < hi[mt][i]) ? z : -INFINITY;
+          s[j][e] = (key >= lo[i] && key < hi[i]) ? z : -INFINITY;
         }
+      uint32_t pf[4];
       float alpha[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        float mx = fmaxf(fmaxf(s[mt][0][2 * i], s[mt][0][2 * i + 1]), fmaxf(s[mt][1][2 * i], s[mt][1][2 * i + 1]));
+        float mx = fmaxf(fmaxf(s[0][2 * i], s[0][2 * i + 1]), fmaxf(s[1][2 * i], s[1][2 * i + 1]));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const float mnew = fmaxf(m[mt][i], mx);
-        alpha[i] = mnew == m[mt][i] ? 1.f : ex2_approx(m[mt][i] - mnew);  // 0 from -inf
-        m[mt][i] = mnew;
+        const float mnew = fmaxf(m[i], mx);
+        alpha[i] = mnew == m[i] ? 1.f : ex2_approx(m[i] - mnew);  // 0 from -inf
+        m[i] = mnew;
         const float mref = mnew == -INFINITY ? 0.f : mnew;
         float sum = 0.f;
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float p0 = ex2_approx(s[mt][j][2 * i] - mref), p1 = ex2_approx(s[mt][j][2 * i + 1] - mref);
+          const float p0 = ex2_approx(s[j][2 * i] - mref), p1 = ex2_approx(s[j][2 * i + 1] - mref);
           sum += p0 + p1;
-          pf[mt][2 * j + i] = pack_bf16x2(p0, p1);  // A fragment of P (rounded to bf16 as V is; the sum is not)
+          pf[2 * j + i] = pack_bf16x2(p0, p1);  // A fragment of P (rounded to bf16 as V is; the sum is not)
         }
-        l[mt][i] = l[mt][i] * alpha[i] + sum;
+        l[i] = l[i] * alpha[i] + sum;
       }
       if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
 #pragma unroll
         for (int d = 0; d < D / 8; ++d) {
-          acc[mt][d][0] *= alpha[0];
-          acc[mt][d][1] *= alpha[0];
-          acc[mt][d][2] *= alpha[1];
-          acc[mt][d][3] *= alpha[1];
+          acc[d][0] *= alpha[0];
+          acc[d][1] *= alpha[0];
+          acc[d][2] *= alpha[1];
+          acc[d][3] *= alpha[1];
         }
       }
-    }
-    // O += P V
+      // O += P V
 #pragma unroll
-    for (int d2 = 0; d2 < D / 16; ++d2) {
-      const int key = (((lane >> 3) & 1) << 3) + (lane & 7), ch = d2 * 2 + (lane >> 4);
-      uint32_t b[4];
-      ldsm4_t(sv + key * (D * 2) + ((ch ^ (key & 7)) << 4), b);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        mma16816(acc[mt][2 * d2], pf[mt], b[0], b[1]);
-        mma16816(acc[mt][2 * d2 + 1], pf[mt], b[2], b[3]);
+      for (int d2 = 0; d2 < D / 16; ++d2) {
+        const int key = (((lane >> 3) & 1) << 3) + (lane & 7), ch = d2 * 2 + (lane >> 4);
+        uint32_t b[4];
+        ldsm4_t(sv + key * (D * 2) + ((ch ^ (key & 7)) << 4), b);
+        mma16816(acc[2 * d2], pf, b[0], b[1]);
+        mma16816(acc[2 * d2 + 1], pf, b[2], b[3]);
       }
+      __syncwarp();
     }
-    __syncwarp();
-  }
-  cp_async_wait<0>();
-  __syncthreads();  // every ring is done with: the warps' sums go over them
+    cp_async_wait<0>();
+    __syncthreads();  // every ring is done with: the warps' sums go over them
 
-  float* const sums = reinterpret_cast<float*>(smem_rows) + static_cast<int64_t>(warp) * C::kRows * D;
-#pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
+    float* const sums = reinterpret_cast<float*>(smem_rows) + warp * kChunkRows * D;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-      float sum = l[mt][i];
+      float sum = l[i];
       sum += __shfl_xor_sync(0xffffffffu, sum, 1);
       sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      const int r = mt * 16 + (lane >> 2) + 8 * i;
-      if ((lane & 3) == 0) ml_s[warp][r] = make_float2(m[mt][i], sum);
+      const int r = (lane >> 2) + 8 * i;
+      if ((lane & 3) == 0) ml_s[warp][r] = make_float2(m[i], sum);
 #pragma unroll
       for (int d = 0; d < D / 8; ++d)
-        *reinterpret_cast<float2*>(sums + r * D + d * 8 + (lane & 3) * 2) =
-            make_float2(acc[mt][d][2 * i], acc[mt][d][2 * i + 1]);
+        *reinterpret_cast<float2*>(sums + r * D + d * 8 + (lane & 3) * 2) = make_float2(acc[d][2 * i], acc[d][2 * i + 1]);
     }
-  __syncthreads();
-  // merge the warps: thread -> (row, four columns)
-  constexpr int kCols = D / 4;
-  const float* const all = reinterpret_cast<const float*>(smem_rows);
-  const int64_t seg = pc.seg0 + static_cast<int64_t>(pc.i) * pc.sp.rts;
-  for (int e = threadIdx.x; e < C::kRows * kCols; e += kRowThreads) {
-    const int r = e / kCols, c4 = (e % kCols) * 4;
-    if (row0 + r >= rows) break;
-    float M = -INFINITY;
+    __syncthreads();
+    // merge the warps: thread -> (row, four columns)
+    constexpr int kCols = D / 4;
+    const float* const all = reinterpret_cast<const float*>(smem_rows);
+    for (int e = threadIdx.x; e < kChunkRows * kCols; e += kRowThreads) {
+      const int r = e / kCols, c4 = (e % kCols) * 4;
+      if (row0 + r >= rows) break;
+      float M = -INFINITY;
 #pragma unroll
-    for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, ml_s[w][r].x);
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float L = 0.f;
+      for (int w = 0; w < kRowWarps; ++w) M = fmaxf(M, ml_s[w][r].x);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      float L = 0.f;
 #pragma unroll
-    for (int w = 0; w < kRowWarps; ++w) {
-      const float2 ml = ml_s[w][r];
+      for (int w = 0; w < kRowWarps; ++w) {
+        const float2 ml = ml_s[w][r];
+        const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+        const float4 a = *reinterpret_cast<const float4*>(all + (w * kChunkRows + r) * D + c4);
+        o.x = fmaf(a.x, f, o.x);
+        o.y = fmaf(a.y, f, o.y);
+        o.z = fmaf(a.z, f, o.z);
+        o.w = fmaf(a.w, f, o.w);
+        L = fmaf(ml.y, f, L);
+      }
+      if (pc.whole) {
+        const int t = (row0 + r) / p.G, h = pc.hk * p.G + (row0 + r) - t * p.G;
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        store4(p, static_cast<int64_t>(q0) + t, h, c4, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+        if (p.lse && c4 == 0) p.lse[static_cast<int64_t>(h) * p.total_q + q0 + t] = lse_of(M, L);
+      } else {
+        const int64_t at = static_cast<int64_t>(pc.place) * kChunkRows + r;
+        *reinterpret_cast<float4*>(p.ws_o + at * D + c4) = o;
+        if (c4 == 0) p.ws_ml[at] = make_float2(M, L);
+      }
+    }
+    __syncthreads();  // the sums and the piece are read
+  }
+  // Nothing here reads what the tile kernel before this one writes, but the join
+  // behind waits for this kernel only: so this one does not end before that one.
+  grid_wait();
+}
+
+// Join the pieces of the cut units: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
+// A unit of P pieces has P - 1 cuts, and each takes its share of the unit's rows (so
+// every cut has about as much to join); `part` of `parts` blocks of a cut takes some of
+// those.  Few pieces: a warp a row.  Many (a long sequence has hundreds): the
+// block's warps share the pieces of a row, since one after the other their latencies
+// would add up.  The order of the sums depends on the number of pieces alone.
+constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps, kJoinFew = 8;
+
+template <int D>
+struct JoinShared {
+  float o[kJoinWarps][D];
+  float l[kJoinWarps];
+};
+
+template <int D, int R>
+__device__ __forceinline__ void join_cut(const ChunkParams& p, int cut, int part, int parts, JoinShared<D>* sh) {
+  const Cut c = static_cast<const Cut*>(p.ws_cuts)[cut];
+  if (c.pieces == 0) return;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  constexpr int kV = D / 32;  // columns a lane
+  const int row0 = c.rt * R, n = min(R, c.rows - row0), cuts = c.pieces - 1;
+  const int first = cut - 1 - c.index;  // the block that starts the unit (its odd place); the others' even ones
+  const int ra = n * c.index / cuts, rb = n * (c.index + 1) / cuts;
+  auto place = [&](int i, int r) { return static_cast<int64_t>(i == 0 ? 2 * first + 1 : 2 * (first + i)) * R + r; };
+  auto load = [&](int64_t at, float (&a)[kV]) {
+    if constexpr (kV == 4) {
+      const float4 v = *reinterpret_cast<const float4*>(p.ws_o + at * D + lane * 4);
+      a[0] = v.x; a[1] = v.y; a[2] = v.z; a[3] = v.w;
+    } else {
+      const float2 v = *reinterpret_cast<const float2*>(p.ws_o + at * D + lane * 2);
+      a[0] = v.x; a[1] = v.y;
+    }
+  };
+  auto store = [&](int r, const float (&o)[kV], float M, float L) {
+    const int t = (row0 + r) / p.G, h = c.hk * p.G + (row0 + r) - t * p.G;
+    const int64_t tok = static_cast<int64_t>(c.q0) + t;
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + tok * p.o_ss + static_cast<int64_t>(h) * p.o_sh + lane * kV);
+    if constexpr (kV == 4)
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack_bf16x2(o[0] * inv, o[1] * inv), pack_bf16x2(o[2] * inv, o[3] * inv));
+    else
+      *dst = pack_bf16x2(o[0] * inv, o[1] * inv);
+    if (p.lse && lane == 0) p.lse[static_cast<int64_t>(h) * p.total_q + tok] = lse_of(M, L);
+  };
+  if (c.pieces <= kJoinFew) {
+    for (int r = ra + part * kJoinWarps + warp; r < rb; r += parts * kJoinWarps) {
+      // lane i holds piece i's maximum and sum; a piece that saw no key of this row left zeros
+      const float2 ml = lane < c.pieces ? p.ws_ml[place(lane, r)] : make_float2(-INFINITY, 0.f);
+      float a[kJoinFew][kV];
+#pragma unroll
+      for (int i = 0; i < kJoinFew; ++i)
+        if (i < c.pieces) load(place(i, r), a[i]);
+      float M = ml.x;
+#pragma unroll
+      for (int d = 4; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+      M = __shfl_sync(0xffffffffu, M, 0);
       const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
-      const float4 a = *reinterpret_cast<const float4*>(all + (static_cast<int64_t>(w) * C::kRows + r) * D + c4);
-      o.x = fmaf(a.x, f, o.x);
-      o.y = fmaf(a.y, f, o.y);
-      o.z = fmaf(a.z, f, o.z);
-      o.w = fmaf(a.w, f, o.w);
+      float o[kV] = {}, L = 0.f;
+#pragma unroll
+      for (int i = 0; i < kJoinFew; ++i)
+        if (i < c.pieces) {
+          const float fi = __shfl_sync(0xffffffffu, f, i);
+          L = fmaf(__shfl_sync(0xffffffffu, ml.y, i), fi, L);
+#pragma unroll
+          for (int v = 0; v < kV; ++v) o[v] = fmaf(a[i][v], fi, o[v]);
+        }
+      store(r, o, M, L);
+    }
+    return;
+  }
+  for (int r = ra + part; r < rb; r += parts) {
+    float M = -INFINITY, L = 0.f;
+    float o[kV] = {};
+    for (int i = lane; i < c.pieces; i += 32) M = fmaxf(M, p.ws_ml[place(i, r)].x);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+#pragma unroll 8
+    for (int i = warp; i < c.pieces; i += kJoinWarps) {
+      const int64_t at = place(i, r);
+      const float2 ml = p.ws_ml[at];
+      const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+      float a[kV];
+      load(at, a);
+#pragma unroll
+      for (int v = 0; v < kV; ++v) o[v] = fmaf(a[v], f, o[v]);
       L = fmaf(ml.y, f, L);
     }
-    if (pc.nseg == 1) {
-      const int t = (row0 + r) / p.G, h = pc.hk * p.G + (row0 + r) - t * p.G;
-      const float inv = L > 0.f ? 1.f / L : 0.f;
-      store4(p, static_cast<int64_t>(q0) + t, h, c4, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-      if (p.lse && c4 == 0) p.lse[static_cast<int64_t>(h) * p.total_q + q0 + t] = lse_of(M, L);
-    } else if (seg < p.max_segs) {
-      *reinterpret_cast<float4*>(p.ws_o + (seg * C::kRows + r) * D + c4) = o;
-      if (c4 == 0) p.ws_ml[seg * C::kRows + r] = make_float2(M, L);
+    __syncthreads();  // the sums of the row before are read
+#pragma unroll
+    for (int v = 0; v < kV; ++v) sh->o[warp][lane * kV + v] = o[v];
+    if (lane == 0) sh->l[warp] = L;
+    __syncthreads();
+    if (warp == 0) {
+      L = 0.f;
+#pragma unroll
+      for (int v = 0; v < kV; ++v) o[v] = 0.f;
+#pragma unroll
+      for (int x = 0; x < kJoinWarps; ++x) {
+        L += sh->l[x];
+#pragma unroll
+        for (int v = 0; v < kV; ++v) o[v] += sh->o[x][lane * kV + v];
+      }
+      store(r, o, M, L);
     }
   }
 }
 
-// Join the pieces of a unit: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i,
-// always in the order of the pieces.  A block takes 16 rows (blockIdx.y) of one unit.
-template <int D, int R, int T>
-__global__ void __launch_bounds__(128) k_chunk_join(const ChunkParams p) {
-  __shared__ Piece pc_s;
-  __shared__ int64_t warp_sums[4];
-  if (!find_piece<R, T>(p, blockIdx.x, true, &pc_s, warp_sums)) return;
-  const Piece& pc = pc_s;
-  if (pc.nseg == 1) return;  // written by its only piece
-  const int rows = pc.sp.q_len * p.G, row0 = pc.rt * R;
-  constexpr int kCols = D / 4;
-  for (int e = threadIdx.x; e < 16 * kCols; e += 128) {
-    const int r = blockIdx.y * 16 + e / kCols, c4 = (e % kCols) * 4;
-    if (row0 + r >= rows) break;
-    float M = -INFINITY;
-    for (int i = 0; i < pc.nseg; ++i) {
-      const int64_t seg = pc.seg0 + static_cast<int64_t>(i) * pc.sp.rts;
-      if (seg < p.max_segs) M = fmaxf(M, p.ws_ml[seg * R + r].x);
-    }
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    float L = 0.f;
-#pragma unroll 4
-    for (int i = 0; i < pc.nseg; ++i) {
-      const int64_t seg = pc.seg0 + static_cast<int64_t>(i) * pc.sp.rts;
-      if (seg >= p.max_segs) break;
-      const float2 ml = p.ws_ml[seg * R + r];
-      const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
-      const float4 a = *reinterpret_cast<const float4*>(p.ws_o + (seg * R + r) * D + c4);
-      o.x = fmaf(a.x, f, o.x);
-      o.y = fmaf(a.y, f, o.y);
-      o.z = fmaf(a.z, f, o.z);
-      o.w = fmaf(a.w, f, o.w);
-      L = fmaf(ml.y, f, L);
-    }
-    const int t = (row0 + r) / p.G, h = pc.hk * p.G + (row0 + r) - t * p.G;
-    const float inv = L > 0.f ? 1.f / L : 0.f;
-    store4(p, static_cast<int64_t>(pc.sp.q0) + t, h, c4, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-    if (p.lse && c4 == 0) p.lse[static_cast<int64_t>(h) * p.total_q + pc.sp.q0 + t] = lse_of(M, L);
-  }
+// Blocks [0, tile_blocks) join the tile kernel's units, the others the row kernel's.
+constexpr int kJoinTileParts = 8, kJoinRowParts = 1;
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads)
+    k_chunk_join(const ChunkParams row, const ChunkParams tile, int tile_blocks) {
+  __shared__ JoinShared<D> sh;
+  grid_wait();  // every block: what follows this kernel relies on the ones before it
+  const int b = blockIdx.x, c = b - tile_blocks;
+  if (b < tile_blocks) join_cut<D, kChunkTileRows>(tile, 1 + b / kJoinTileParts, b % kJoinTileParts, kJoinTileParts, &sh);
+  else join_cut<D, kChunkRows>(row, 1 + c / kJoinRowParts, c % kJoinRowParts, kJoinRowParts, &sh);
 }
 
 // ----------------------------------------------------------------------------
 // launchers (host)
 // ----------------------------------------------------------------------------
-cudaError_t launch_chunk_join(const ChunkParams& p, int rows, int keys, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(p.max_units), static_cast<unsigned>(rows / 16));
-  const bool wide = p.D == 128;
-  if (rows == 16 && keys == kRowKeys) {
-    if (wide) k_chunk_join<128, 16, kRowKeys><<<grid, 128, 0, s>>>(p);
-    else k_chunk_join<64, 16, kRowKeys><<<grid, 128, 0, s>>>(p);
-  } else if (rows == 32 && keys == kRowKeys) {
-    if (wide) k_chunk_join<128, 32, kRowKeys><<<grid, 128, 0, s>>>(p);
-    else k_chunk_join<64, 32, kRowKeys><<<grid, 128, 0, s>>>(p);
-  } else if (rows == kChunkTileRows && keys == kTile) {
-    if (wide) k_chunk_join<128, kChunkTileRows, kTile><<<grid, 128, 0, s>>>(p);
-    else k_chunk_join<64, kChunkTileRows, kTile><<<grid, 128, 0, s>>>(p);
-  } else {
-    return cudaErrorInvalidValue;
-  }
-  return cudaGetLastError();
+// A launch that may start while the kernel before it still runs (grid_trigger).
+template <typename K, typename... A>
+static cudaError_t launch_dependent(K kernel, unsigned grid, int threads, int smem, bool dependent, cudaStream_t s,
+                                    const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = dependent ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-template <int D, int MT, bool kScore>
-static cudaError_t launch_rows_one(const ChunkParams& p, cudaStream_t s) {
-  using C = RowCfg<D, MT>;
+cudaError_t launch_chunk_join(const ChunkParams& row, const ChunkParams& tile, cudaStream_t s) {
+  const int tile_blocks = tile.slots > 1 ? (tile.slots - 1) * kJoinTileParts : 0;
+  const int row_blocks = row.slots > 1 ? (row.slots - 1) * kJoinRowParts : 0;
+  if (tile_blocks + row_blocks == 0) return cudaSuccess;
+  const unsigned blocks = static_cast<unsigned>(tile_blocks + row_blocks);
+  if (row.D == 64) return launch_dependent(k_chunk_join<64>, blocks, kJoinThreads, 0, true, s, row, tile, tile_blocks);
+  return launch_dependent(k_chunk_join<128>, blocks, kJoinThreads, 0, true, s, row, tile, tile_blocks);
+}
+
+template <int D, bool kScore>
+static cudaError_t launch_rows_one(const ChunkParams& p, bool after_tiles, cudaStream_t s) {
   static DeviceOnce once;
   cudaError_t e = once.run([] {
-    return cudaFuncSetAttribute(k_chunk_rows<D, MT, kScore>, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    return cudaFuncSetAttribute(k_chunk_rows<D, kScore>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                RowCfg<D>::kSmem);
   });
   if (e != cudaSuccess) return e;
-  k_chunk_rows<D, MT, kScore><<<p.max_segs, kRowThreads, C::kSmem, s>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  return launch_chunk_join(p, C::kRows, kRowKeys, s);
+  return launch_dependent(k_chunk_rows<D, kScore>, static_cast<unsigned>(p.slots), kRowThreads, RowCfg<D>::kSmem,
+                          after_tiles, s, p);
 }
 
-template <int D, int MT>
-static cudaError_t launch_rows_mt(const ChunkParams& p, cudaStream_t s) {
-  return (p.score.c1 != 0.f || p.score.slopes) ? launch_rows_one<D, MT, true>(p, s)
-                                               : launch_rows_one<D, MT, false>(p, s);
-}
-
-cudaError_t launch_chunk_rows(const ChunkParams& p, int row_tiles, cudaStream_t s) {
-  if (p.max_segs <= 0 || p.max_units <= 0) return cudaSuccess;
-  if (p.D == 64) return row_tiles == 1 ? launch_rows_mt<64, 1>(p, s) : launch_rows_mt<64, 2>(p, s);
-  return row_tiles == 1 ? launch_rows_mt<128, 1>(p, s) : launch_rows_mt<128, 2>(p, s);
+cudaError_t launch_chunk_rows(const ChunkParams& p, bool after_tiles, cudaStream_t s) {
+  const bool shaped = p.score.c1 != 0.f || p.score.slopes;
+  if (p.D == 64) return shaped ? launch_rows_one<64, true>(p, after_tiles, s) : launch_rows_one<64, false>(p, after_tiles, s);
+  return shaped ? launch_rows_one<128, true>(p, after_tiles, s) : launch_rows_one<128, false>(p, after_tiles, s);
 }
 
 }  // namespace bfa

@@ -11,6 +11,10 @@
 
 namespace bfa {
 
+constexpr int kChunkTileRows = 256;  // rows of a unit of launch_chunk_tiles
+constexpr int kChunkRows = 16;       // rows of a unit of launch_chunk_rows
+constexpr int kChunkCutBytes = 24;   // a note of a cut (chunk_split.cuh)
+
 struct ChunkParams {
   int32_t D, H, Hkv, G;  // G = H / Hkv query heads a kv head
   int32_t B;             // sequences
@@ -32,24 +36,24 @@ struct ChunkParams {
   float scale_log2;            // softmax scale * log2(e)
   ScoreParams score;
   // which sequences this launch serves: rows = new tokens * G in (rows_lo, rows_hi]
-  int64_t rows_lo, rows_hi;
-  // split of the keys: about `slots` pieces of at least `min_tiles` key tiles
-  int32_t slots, min_tiles;
-  int32_t max_segs;   // pieces the grid and the workspace have room for
-  int32_t max_units;  // (sequence, kv head, row tile) units there can be
-  float* ws_o;        // [max_segs, rows of a tile, D] partial outputs, unnormalised
-  float2* ws_ml;      // [max_segs, rows of a tile] reference maximum (log2) and sum
+  int32_t rows_lo, rows_hi;
+  // split of the work (chunk_split.cuh): blocks, the least share of one, and the length
+  // that starting a unit counts, in key tiles
+  int32_t slots, min_share, start_cost;
+  float* ws_o;   // [2 slots, rows of a unit, D] partial outputs, unnormalised
+  float2* ws_ml; // [2 slots, rows of a unit] reference maximum (log2) and sum
+  void* ws_cuts; // [slots] Cut
   uint64_t wait_ns;
   uint32_t* err;
 };
 
-// few rows a kv head: 16 or 32 rows a unit (row_tiles 1, 2); with the join
-cudaError_t launch_chunk_rows(const ChunkParams& p, int row_tiles, cudaStream_t s);
-// many rows: 256 rows a unit; with the join
+// many rows a kv head: 256 rows a unit
 cudaError_t launch_chunk_tiles(const CUtensorMap& tk, const CUtensorMap& tv, const ChunkParams& p, cudaStream_t s);
-// joins the pieces of units of `rows` rows and key tiles of `keys`
-cudaError_t launch_chunk_join(const ChunkParams& p, int rows, int keys, cudaStream_t s);
+// few rows: 16 rows a unit; `after_tiles`: launched behind the tile kernel, whose
+// last blocks it may overlap
+cudaError_t launch_chunk_rows(const ChunkParams& p, bool after_tiles, cudaStream_t s);
+// joins the cut units of both (slots = 0: that one was not launched)
+cudaError_t launch_chunk_join(const ChunkParams& row, const ChunkParams& tile, cudaStream_t s);
 
-constexpr int kChunkTileRows = 256;  // rows of a unit of launch_chunk_tiles
 
 }  // namespace bfa

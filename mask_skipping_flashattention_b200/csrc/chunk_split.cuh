@@ -1,13 +1,24 @@
-// How the chunk kernels divide a ragged batch, computed by every block from the
-// lengths on the device, so that the host needs none of them.
+// How the chunk kernels divide a ragged batch, computed on the device from the
+// lengths there, so that the host needs none of them.
 //
 // A unit is (sequence, kv head, row tile): R rows of the sequence's new tokens x
-// the G heads of the kv head (row r = token r / G, head r % G).  Its keys, the
-// tiles from the first that any new token sees to the last, are cut into pieces of
-// nearly equal length; a block computes one piece.  The piece length is the
-// batch's whole work over `slots`, so that few long sequences fill the machine as
-// many short ones do.  Pieces are numbered by sequence, kv head, piece, row tile
-// (the row tiles of one key range run together and share it in L2).
+// the G heads of the kv head (row r = token r / G, head r % G), with the key tiles
+// (T keys) that some row of it sees.  The units in order (row tiles fastest) make
+// one line of work, a unit's length being its key tiles plus a constant for starting
+// it; block b of `slots` resident ones takes the b-th of equal shares, at least
+// min_share long.  So every block has the same work whatever the batch looks like (one
+// long sequence, many short ones, a causal triangle), and at most slots - 1 units are
+// cut.  A block's part of a cut unit goes to the workspace: place 2 b if it starts
+// inside the unit, 2 b + 1 if it starts it; and block b leaves a note of the cut in
+// front of it, by which the join finds what to do.
+// Measured on single tokens (8 kv heads, D 128) against blocks that each look up one of
+// many pieces: 64 ragged sequences of up to 8192 keys 203 us in pieces of a length chosen
+// by a cost model, and a call of one short sequence spent 9 us in blocks with nothing
+// to do.
+//
+// The order along a unit's line only has to be the same everywhere, so lengths are a
+// closed form of the row tile (line_before) and a cut at x of w falls on key tile
+// n x / w of the unit's own n.
 #pragma once
 
 #include <cstdint>
@@ -17,115 +28,199 @@
 namespace bfa {
 
 struct SeqSpan {
-  int32_t q0, q_len;   // rows of q
-  int32_t kv;          // keys
-  int32_t t_lo, n;     // first key tile and tiles (at least 1) of the whole chunk
-  int32_t rts;         // row tiles; 0: not served by this launch
+  int32_t q0, q_len;  // rows of q
+  int32_t kv;         // keys
+  int32_t rts;        // row tiles; 0: not served by this launch
 };
 
 struct Piece {
   SeqSpan sp;
   int32_t s, hk, rt;
-  int32_t t0, t1;      // key tiles
-  int32_t nseg, i;     // pieces of the unit, this one's index
-  int64_t seg0;        // piece i of the unit is number seg0 + i * sp.rts
+  int32_t lo, hi;     // keys some row of the unit sees
+  int32_t t0, t1;     // key tiles of the piece
+  int32_t whole;      // the piece is its unit
+  int32_t place;      // its place in the workspace otherwise
 };
 
-template <int R, int T>
+// The cut between blocks b - 1 and b, for the join.
+struct Cut {
+  int32_t pieces;      // pieces of the unit it goes through; 0: it goes through none
+  int32_t index;       // number of this cut among the unit's
+  int32_t hk, rt, q0;  // the unit; first row of its sequence in q
+  int32_t rows;        // rows of its sequence's chunk (a kv head)
+};
+static_assert(sizeof(Cut) == kChunkCutBytes, "workspace size");
+
+template <int R>
 __device__ __forceinline__ SeqSpan seq_span(const ChunkParams& p, int s) {
   SeqSpan sp;
   // lengths outside their arrays are cut to them
-  int a = min(max(__ldg(p.cu_seqlens + s), 0), p.total_q);
-  int b = min(max(__ldg(p.cu_seqlens + s + 1), a), p.total_q);
+  const int a = min(max(__ldg(p.cu_seqlens + s), 0), p.total_q);
+  const int b = min(max(__ldg(p.cu_seqlens + s + 1), a), p.total_q);
   sp.q0 = a;
   sp.q_len = b - a;
-  const int64_t room = static_cast<int64_t>(p.pages_per_seq) * p.page_size;
-  sp.kv = static_cast<int>(min(static_cast<int64_t>(max(__ldg(p.seqused_k + s), 0)), room));
-  const int64_t rows = static_cast<int64_t>(sp.q_len) * p.G;
-  sp.rts = (rows > p.rows_lo && rows <= p.rows_hi) ? static_cast<int>((rows + R - 1) / R) : 0;
-  int lo = p.window >= 0 ? max(0, sp.kv - sp.q_len - p.window + 1) : 0;
-  lo = min(lo, sp.kv);
-  sp.t_lo = lo / T;
-  sp.n = max(1, (sp.kv + T - 1) / T - sp.t_lo);
+  sp.kv = min(max(__ldg(p.seqused_k + s), 0), p.pages_per_seq * p.page_size);  // below 2^30
+  const int rows = sp.q_len * p.G;                                              // below 2^23
+  sp.rts = (rows > p.rows_lo && rows <= p.rows_hi) ? (rows + R - 1) / R : 0;
   return sp;
 }
 
-// Inclusive scan over the block's threads (a multiple of 32, at most 512).
-__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums, int64_t& total) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) {
-    const int64_t x = __shfl_up_sync(0xffffffffu, v, d);
-    if (lane >= d) v += x;
-  }
-  __syncthreads();  // the sums of a scan before may still be read
-  if (lane == 31) warp_sums[warp] = v;
-  __syncthreads();
-  int64_t before = 0;
-  total = 0;
-  for (int w = 0; w < warps; ++w) {
-    const int64_t x = warp_sums[w];
-    if (w < warp) before += x;
-    total += x;
-  }
-  return v + before;
+// length of the line before row tile rt of a sequence's kv head
+template <int R, int T>
+__device__ __forceinline__ int64_t line_before(const ChunkParams& p, const SeqSpan& sp, unsigned rt) {
+  const unsigned reach = p.window >= 0 ? min(sp.kv, p.window + sp.q_len) : sp.kv;  // keys of the whole chunk
+  if (R == kChunkRows || p.window >= 0)  // every unit alike
+    return static_cast<int64_t>(rt) * (reach / T + 1 + p.start_cost);
+  // causal: unit i sees the keys before the chunk and R (i + 1) / G tokens of it (R = 2 T;
+  // row tiles stay below 2^15)
+  const unsigned before = max(sp.kv - sp.q_len, 0);
+  return static_cast<int64_t>(rt) * (before / T + 1 + p.start_cost) + rt * (rt + 1u) / p.G;
 }
 
-// The piece `want` (or, with `units`, the unit `want` as a piece with i = 0) into
-// shared memory; false when there is none.  Called by the whole block.
+// The line's length and the share of a block.
+struct Line {
+  int64_t total, share;
+};
+
+// Called by one whole warp (lanes = sequences).
 template <int R, int T>
-__device__ bool find_piece(const ChunkParams& p, int64_t want, bool units, Piece* out, int64_t* warp_sums) {
-  const int tid = threadIdx.x, nt = blockDim.x;
-  int64_t work = 0, total = 0;
+__device__ __forceinline__ Line line_of(const ChunkParams& p) {
+  const int lane = threadIdx.x & 31;
+  int64_t sum = 0;
+#pragma unroll 1
+  for (int s = lane; s < p.B; s += 32) {
+    const SeqSpan sp = seq_span<R>(p, s);
+    sum += line_before<R, T>(p, sp, sp.rts) * p.Hkv;
+  }
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+  Line ln;
+  ln.total = sum;
+  // ceil(total / slots) in 32 bits (rounded up by at most 2^-16 of itself for lines past 2^32)
+  const unsigned hi = static_cast<unsigned>(sum >> 32), slots = p.slots;
+  const int64_t even = hi ? (static_cast<int64_t>(static_cast<unsigned>(sum >> 16) / slots) + 1) << 16
+                          : (static_cast<unsigned>(sum) + (slots - 1u)) / slots;
+  ln.share = max(static_cast<int64_t>(p.min_share), even);
+  return ln;
+}
+
+// A place on the line: offset x of w in unit (s, hk, rt).
+struct Walk {
   SeqSpan sp;
-  for (int base = 0; base < p.B; base += nt) {
-    int64_t w = 0;
-    if (base + tid < p.B) {
-      sp = seq_span<R, T>(p, base + tid);
-      w = static_cast<int64_t>(sp.n) * sp.rts * p.Hkv;
-    }
-    block_scan(w, warp_sums, total);
-    work += total;
+  int32_t s, hk, rt;
+  int64_t x, w;
+  template <int R, int T>
+  __device__ __forceinline__ void set_unit(const ChunkParams& p) {
+    w = line_before<R, T>(p, sp, rt + 1) - line_before<R, T>(p, sp, rt);
+    x = 0;
   }
-  const int64_t per = max(static_cast<int64_t>(p.min_tiles), (work + p.slots - 1) / p.slots);
-  int64_t done_units = 0, done_segs = 0;
-  __shared__ int found;
-  if (tid == 0) found = 0;
-  for (int base = 0; base < p.B; base += nt) {
-    int64_t nu = 0, ns = 0;
-    int nseg = 1;
-    if (base + tid < p.B) {
-      if (p.B > nt) sp = seq_span<R, T>(p, base + tid);
-      nseg = static_cast<int>((sp.n + per - 1) / per);
-      nu = static_cast<int64_t>(sp.rts) * p.Hkv;
-      ns = nu * nseg;
+  // the next unit; false at the end of the batch
+  template <int R, int T>
+  __device__ __forceinline__ bool next(const ChunkParams& p) {
+    if (++rt == sp.rts) {
+      rt = 0;
+      if (++hk == p.Hkv) {
+        hk = 0;
+        do {
+          if (++s >= p.B) return false;
+          sp = seq_span<R>(p, s);
+        } while (sp.rts == 0);
+      }
     }
-    int64_t units_here, segs_here;
-    const int64_t eu = done_units + block_scan(nu, warp_sums, units_here) - nu;
-    const int64_t es = done_segs + block_scan(ns, warp_sums, segs_here) - ns;
-    const int64_t e = units ? eu : es, cnt = units ? nu : ns;
-    if (want >= e && want < e + cnt) {
-      Piece pc;
-      pc.sp = sp;
-      pc.s = base + tid;
-      pc.nseg = nseg;
-      const int64_t local = want - e;
-      pc.rt = static_cast<int>(local % sp.rts);
-      const int64_t rest = local / sp.rts;
-      pc.i = units ? 0 : static_cast<int>(rest % nseg);
-      pc.hk = static_cast<int>(units ? rest : rest / nseg);
-      pc.t0 = sp.t_lo + static_cast<int>(static_cast<int64_t>(sp.n) * pc.i / nseg);
-      pc.t1 = sp.t_lo + static_cast<int>(static_cast<int64_t>(sp.n) * (pc.i + 1) / nseg);
-      pc.seg0 = es + (static_cast<int64_t>(pc.hk) * nseg) * sp.rts + pc.rt;
-      *out = pc;
-      found = 1;
-    }
-    done_units += units_here;
-    done_segs += segs_here;
-    if (want < (units ? done_units : done_segs)) break;  // the same for every thread
+    set_unit<R, T>(p);
+    return true;
   }
-  __syncthreads();
-  return found != 0;
+};
+
+// The unit at `pos` (below the line's length).  Called by one whole warp.
+template <int R, int T>
+__device__ __forceinline__ Walk walk_to(const ChunkParams& p, int64_t pos) {
+  constexpr unsigned kAll = 0xffffffffu;
+  const int lane = threadIdx.x & 31;
+  Walk k;
+  k.s = 0;
+#pragma unroll 1
+  for (int base = 0;; base += 32) {
+    int64_t len = 0;
+    if (base + lane < p.B) {
+      const SeqSpan sp = seq_span<R>(p, base + lane);
+      len = line_before<R, T>(p, sp, sp.rts) * p.Hkv;
+    }
+    int64_t end = len;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t x = __shfl_up_sync(kAll, end, d);
+      if (lane >= d) end += x;
+    }
+    const unsigned past = __ballot_sync(kAll, pos < end);
+    if (past || base + 32 >= p.B) {  // the second only guards against lengths that change under the call
+      const int at = past ? __ffs(past) - 1 : min(31, p.B - 1 - base);
+      k.s = base + at;
+      pos -= __shfl_sync(kAll, end - len, at);
+      break;
+    }
+    pos -= __shfl_sync(kAll, end, 31);
+  }
+  k.sp = seq_span<R>(p, k.s);
+  const int64_t head = line_before<R, T>(p, k.sp, k.sp.rts);
+  k.hk = 0;
+  while (k.hk + 1 < p.Hkv && pos >= head) {
+    pos -= head;
+    ++k.hk;
+  }
+  int a = 0, b = max(k.sp.rts, 1);  // the last row tile in [a, b) with line_before <= pos
+#pragma unroll 1
+  while (b - a > 1) {
+    const int mid = (a + b) >> 1;
+    if (line_before<R, T>(p, k.sp, mid) <= pos) a = mid;
+    else b = mid;
+  }
+  k.rt = a;
+  const int64_t before = line_before<R, T>(p, k.sp, a);
+  k.template set_unit<R, T>(p);
+  k.x = min(pos - before, k.w - 1);
+  return k;
+}
+
+// The cut in front of block b, whose share starts at k (k.w = 0: it has none).
+__device__ __forceinline__ void note_cut(const ChunkParams& p, const Walk& k, int64_t share, int b, bool have) {
+  Cut c = {};
+  if (have && k.x > 0) {
+    // cuts before this one, and behind it, a share apart (at most `slots` of them)
+    int before = 0, behind = 0;
+    for (int64_t x = k.x - share; x > 0; x -= share) ++before;
+    for (int64_t x = k.x + share; x < k.w; x += share) ++behind;
+    c.index = before;
+    c.pieces = before + behind + 2;
+    c.hk = k.hk;
+    c.rt = k.rt;
+    c.q0 = k.sp.q0;
+    c.rows = k.sp.q_len * p.G;
+  }
+  static_cast<Cut*>(p.ws_cuts)[b] = c;
+}
+
+// Part [k.x, x1) of the unit at k as a piece of block b.
+template <int R, int T>
+__device__ __forceinline__ Piece piece_of(const ChunkParams& p, const Walk& k, int64_t x1, int b) {
+  Piece pc;
+  pc.sp = k.sp;
+  pc.s = k.s;
+  pc.hk = k.hk;
+  pc.rt = k.rt;
+  const int rows = k.sp.q_len * p.G, row0 = k.rt * R, first = k.sp.kv - k.sp.q_len;
+  const int pos_a = first + row0 / p.G, pos_b = first + (min(row0 + R, rows) - 1) / p.G;
+  pc.lo = p.window >= 0 ? max(0, pos_a - p.window + 1) : 0;
+  pc.hi = min(k.sp.kv, pos_b + 1);
+  const int t_lo = pc.lo / T, n = pc.hi > pc.lo ? (pc.hi + T - 1) / T - t_lo : 0;
+  pc.whole = k.x == 0 && x1 == k.w;
+  pc.place = 2 * b + (k.x == 0 ? 1 : 0);
+  // n x / w: lengths stay far below 2^24, so a float quotient and its truncation are the same for
+  // every block that asks for the same x
+  const float step = static_cast<float>(n) / static_cast<float>(k.w);
+  pc.t0 = t_lo + (k.x == 0 ? 0 : min(n, static_cast<int>(static_cast<float>(k.x) * step)));
+  pc.t1 = t_lo + (x1 == k.w ? n : min(n, static_cast<int>(static_cast<float>(x1) * step)));
+  return pc;
 }
 
 }  // namespace bfa

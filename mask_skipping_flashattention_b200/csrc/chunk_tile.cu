@@ -5,10 +5,11 @@
 // built as it is (fwd.cu: two 128-row slots a CTA that share every key tile,
 // S = Q K^T and O += P V as tcgen05 products with S, P and O in tensor memory, one
 // query row a softmax thread).  What differs:
-//   - a unit is 256 rows (tokens x the G heads of a kv head) of one sequence and
-//     a CTA walks one piece of its key tiles (chunk_split.cuh), cut to the keys that
-//     the unit's rows see; both slots walk all of them, since their rows are at
-//     most 256 / G tokens apart;
+//   - a unit is 256 rows (tokens x the G heads of a kv head) of one sequence with
+//     the key tiles that its rows see, and one CTA a SM stays resident and works off an
+//     equal share of all units' tiles (chunk_split.cuh), at most its first and last
+//     unit in part; both slots walk all tiles, since their rows are at most 256 / G
+//     tokens apart.  The barriers' phases run on from piece to piece;
 //   - Q rows go from global memory into the swizzled tile by the softmax threads,
 //     one row each: any G, any strides, rows past the end as zeros;
 //   - the producer warp loads a tile page by page, one page a lane, with the page
@@ -40,9 +41,9 @@ static_assert(kUnitRows == 2 * kTile, "two slots");
 
 struct TileWork {
   Piece pc;
+  int32_t have;         // 0: no more pieces
   int32_t rows, row0;   // rows of the sequence's chunk (a kv head), first row of the unit
-  int32_t lo, hi;       // keys some row of the unit sees
-  int32_t t0, n;        // first key tile and key tiles of this piece
+  int32_t n;            // key tiles of this piece
   int32_t two;          // slot 1 has rows
 };
 
@@ -69,135 +70,170 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ TileWork wk_s;
-  __shared__ int64_t warp_sums[kThreads / 32];
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   auto sK = [&](int st) { return sK0 + st * C::kTileBytes; };
   auto sV = [&](int st) { return sV0 + st * C::kTileBytes; };
+  // the block between two pieces: nothing of the last one is in flight, the next one is known
+  auto meet = [&]() {
+    tc_fence_before();
+    named_bar_sync(0, kThreads);
+    tc_fence_after();
+  };
 
-  if (!find_piece<kUnitRows, kTile>(p, blockIdx.x, false, &wk_s.pc, warp_sums)) return;
-  if (threadIdx.x == 0) {
-    TileWork& w = wk_s;
-    const Piece& pc = w.pc;
-    abort_flag = 0;
-    for (int i = 0; i < NBAR; ++i) mbar_init(bar(i), i == BQ ? 9 : ((i == BP || i == BP + 1) ? 4 : 1));
-    fence_barrier_init();
-    w.rows = pc.sp.q_len * p.G;
-    w.row0 = pc.rt * kUnitRows;
-    const int first = pc.sp.kv - pc.sp.q_len;  // position of the chunk's first token
-    const int pos_a = first + w.row0 / p.G, pos_b = first + (min(w.row0 + kUnitRows, w.rows) - 1) / p.G;
-    w.lo = p.window >= 0 ? max(0, pos_a - p.window + 1) : 0;
-    w.hi = min(pc.sp.kv, pos_b + 1);
-    w.t0 = max(pc.t0, w.lo / kTile);
-    const int t1 = w.hi > w.lo ? min(pc.t1, (w.hi + kTile - 1) / kTile) : 0;
-    w.n = max(0, t1 - w.t0);
-    w.two = w.row0 + kTile < w.rows;
+  grid_trigger();  // the row kernel, or the join, may take the place of blocks that are done
+  // warp 0 walks this block's share of the line
+  Walk walk;
+  int64_t left = 0;
+  bool more = false;
+  if (warp == 0) {
+    const Line ln = line_of<kUnitRows, kTile>(p);
+    const int64_t pos = ln.share * blockIdx.x;
+    left = min(ln.share, ln.total - pos);
+    more = left > 0;
+    if (more) walk = walk_to<kUnitRows, kTile>(p, pos);
+    if (lane == 0) note_cut(p, walk, ln.share, blockIdx.x, more);
+  }
+  auto post_piece = [&]() {  // warp 0
+    if (more) {
+      const int64_t x1 = min(walk.w, walk.x + left);
+      const Piece pc = piece_of<kUnitRows, kTile>(p, walk, x1, blockIdx.x);
+      left -= x1 - walk.x;
+      if (lane == 0) {
+        wk_s.pc = pc;
+        wk_s.rows = pc.sp.q_len * p.G;
+        wk_s.row0 = pc.rt * kUnitRows;
+        wk_s.n = pc.t1 - pc.t0;
+        wk_s.two = pc.rt * kUnitRows + kTile < pc.sp.q_len * p.G;
+      }
+    }
+    if (lane == 0) wk_s.have = more;
+    more = more && left > 0 && walk.template next<kUnitRows, kTile>(p);
+  };
+  if (warp == 0) {
+    if (lane == 0) {
+      abort_flag = 0;
+      for (int i = 0; i < NBAR; ++i) mbar_init(bar(i), i == BQ ? 9 : ((i == BP || i == BP + 1) ? 4 : 1));
+      fence_barrier_init();
+    }
+    post_piece();
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(&tmem_slot), C::kTmemCols);
     tmem_relinquish();
   }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
+  meet();
   const uint32_t tmem = tmem_slot;
   const TileWork& wk = wk_s;
   const uint64_t cap = p.wait_ns;
-  const int n = wk.n;
+  // what the barriers have seen before this piece: pieces with tiles, tiles (F), commits of E,
+  // tiles of each slot, edge tiles.  Every role counts for itself, all alike.
+  int c_piece = 0, c_f = 0, c_e = 0, c_s1 = 0, c_z = 0;
+  auto count_piece = [&](int n) {
+    if (n > 0) {
+      ++c_piece;
+      c_f += n;
+      c_e += n + 1;
+      c_s1 += wk.two ? n : 0;
+    }
+  };
 
   // a tile with value rows that no row of the unit may read
   auto edge = [&](int j) {
-    const int k0 = (wk.t0 + j) * kTile;
-    return k0 < wk.lo || k0 + kTile > wk.hi;
+    const int k0 = (wk.pc.t0 + j) * kTile;
+    return k0 < wk.pc.lo || k0 + kTile > wk.pc.hi;
   };
 
   if (warp < 4) {
     // ============================================================ warpgroup 0
     regs_dec<kRegsWG0>();
-    if (warp == 0 && n > 0) {
-      // ---------------------------------------------------------- producer
-      // K of the first tile on BQ; at step j, V of tile j and K of tile j + 1 on
-      // F[j & 1] once commit j - 1 has freed both stages.  Lane l loads page l of a
-      // tile (one lane for pages of 128 tokens and more).
-      if (lane == 0) {
-        prefetch_tmap(&tmK);
-        prefetch_tmap(&tmV);
-      }
-      const int box = min(p.page_size, kTile);
-      const int boxes = kTile / box;
-      const int32_t* bt = p.block_table + static_cast<int64_t>(wk.pc.s) * p.pages_per_seq;
-      const int past = static_cast<int>(p.num_pages * p.page_size);  // a row outside the cache reads as zeros
-      // row of the cache of this lane's box of tile j
-      auto place = [&](int j) -> int {
-        const int key = (wk.t0 + j) * kTile + lane * box;
-        if (lane >= boxes || j >= n || key >= wk.hi || key + box <= wk.lo) return past;
-        const int pi = key / p.page_size;
-        const int page = __ldg(bt + pi);
-        return (page < 0 || page >= p.num_pages) ? past : page * p.page_size + (key - pi * p.page_size);
-      };
-      auto load = [&](const CUtensorMap* map, uint8_t* dst, uint32_t b, int row) {
-        if (lane < boxes) {
-#pragma unroll
-          for (int pn = 0; pn < C::kPanels; ++pn)
-            tma_load_4d(smem_u32(dst + pn * 16384 + lane * box * 128), map, b, pn * 64, wk.pc.hk, row, 0);
+    while (wk.have) {
+      const int n = wk.n;
+      if (warp == 0 && n > 0) {
+        // -------------------------------------------------------- producer
+        // K of the first tile on BQ; at step j, V of tile j and K of tile j + 1 on the
+        // stage of j once commit j - 1 has freed both.  Lane l loads page l of a tile (one
+        // lane for pages of 128 tokens and more).
+        if (lane == 0) {
+          prefetch_tmap(&tmK);
+          prefetch_tmap(&tmV);
         }
-      };
-      int row = place(0);
-      if (lane == 0) mbar_expect_tx(bar(BQ), C::kTileBytes);
-      __syncwarp();
-      load(&tmK, sK(0), bar(BQ), row);
-      int row_n = place(1);
-      int last_f[2] = {-1, -1};
-      for (int j = 0; j < n; ++j) {
-        const int row_nn = place(j + 2);
-        bool ok = true;
-        if (lane == 0 && j >= 1) ok = mbar_wait_fast(bar(BE + ((j - 1) & 1)), ((j - 1) >> 1) & 1, cap, &abort_flag);
-        if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
-        const uint32_t f = bar(BF + (j & 1));
-        const bool have_next = j + 1 < n;
-        if (lane == 0) mbar_expect_tx(f, (have_next ? 2 : 1) * C::kTileBytes);
+        const int box = min(p.page_size, kTile);
+        const int boxes = kTile / box;
+        const int32_t* bt = p.block_table + static_cast<int64_t>(wk.pc.s) * p.pages_per_seq;
+        const int past = static_cast<int>(p.num_pages * p.page_size);  // a row outside the cache reads as zeros
+        // row of the cache of this lane's box of tile j
+        auto place = [&](int j) -> int {
+          const int key = (wk.pc.t0 + j) * kTile + lane * box;
+          if (lane >= boxes || j >= n || key >= wk.pc.hi || key + box <= wk.pc.lo) return past;
+          const int pi = key / p.page_size;
+          const int page = __ldg(bt + pi);
+          return (page < 0 || page >= p.num_pages) ? past : page * p.page_size + (key - pi * p.page_size);
+        };
+        auto load = [&](const CUtensorMap* map, uint8_t* dst, uint32_t b, int row) {
+          if (lane < boxes) {
+#pragma unroll
+            for (int pn = 0; pn < C::kPanels; ++pn)
+              tma_load_4d(smem_u32(dst + pn * 16384 + lane * box * 128), map, b, pn * 64, wk.pc.hk, row, 0);
+          }
+        };
+        int row = place(0);
+        if (lane == 0) mbar_expect_tx(bar(BQ), C::kTileBytes);
         __syncwarp();
-        load(&tmV, sV(j & 1), f, row);
-        if (have_next) load(&tmK, sK((j + 1) & 1), f, row_n);
-        last_f[j & 1] = j;
-        row = row_n;
-        row_n = row_nn;
-      }
-      // every copy this CTA issued must land before it can exit
-      if (lane == 0) {
-        mbar_drain(bar(BQ), 0, &abort_flag);
-        for (int b = 0; b < 2; ++b)
-          if (last_f[b] >= 0) mbar_drain(bar(BF + b), (last_f[b] >> 1) & 1, &abort_flag);
-      }
-    } else if (warp == 1) {
-      // ---------------------------------------------------------- MMA issuer (fwd.cu's order)
-      if (lane == 0 && n > 0) {
+        load(&tmK, sK(c_f & 1), bar(BQ), row);
+        int row_n = place(1);
+        int last = -1;
+        for (int j = 0; j < n; ++j) {
+          const int row_nn = place(j + 2);
+          const int f = c_f + j, e = c_e + j - 1;
+          bool ok = true;
+          if (lane == 0 && j >= 1) ok = mbar_wait_fast(bar(BE + (e & 1)), (e >> 1) & 1, cap, &abort_flag);
+          if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) break;
+          const uint32_t fb = bar(BF + (f & 1));
+          const bool have_next = j + 1 < n;
+          if (lane == 0) mbar_expect_tx(fb, (have_next ? 2 : 1) * C::kTileBytes);
+          __syncwarp();
+          load(&tmV, sV(f & 1), fb, row);
+          if (have_next) load(&tmK, sK((f + 1) & 1), fb, row_n);
+          last = f;
+          row = row_n;
+          row_n = row_nn;
+        }
+        // every copy of this piece must land before the block goes on or exits
+        if (lane == 0) {
+          mbar_drain(bar(BQ), c_piece & 1, &abort_flag);
+          if (last > c_f) mbar_drain(bar(BF + ((last - 1) & 1)), ((last - 1) >> 1) & 1, &abort_flag);
+          if (last >= 0) mbar_drain(bar(BF + (last & 1)), (last >> 1) & 1, &abort_flag);
+        }
+        __syncwarp();
+      } else if (warp == 1 && lane == 0 && n > 0) {
+        // -------------------------------------------------------- MMA issuer (fwd.cu's order)
         const uint32_t tS0 = tmem + C::kColS0, tS1 = tmem + C::kColS1;
         const uint32_t tO0 = tmem + C::kColO0, tO1 = tmem + C::kColO1;
         const bool two = wk.two != 0;
-        int z = 0;  // edge tiles so far
-        bool ok = mbar_wait_fast(bar(BQ), 0, cap, &abort_flag);
+        int z = c_z;
+        bool ok = mbar_wait_fast(bar(BQ), c_piece & 1, cap, &abort_flag);
         if (ok) {
           tc_fence_after();
-          issue_s<D>(tS0, sQ0, sK(0));
+          issue_s<D>(tS0, sQ0, sK(c_f & 1));
           umma_commit(bar(BS + 0));
           if (two) {
-            issue_s<D>(tS1, sQ1, sK(0));
+            issue_s<D>(tS1, sQ1, sK(c_f & 1));
             umma_commit(bar(BS + 1));
           }
-          umma_commit(bar(BE + 0));
+          umma_commit(bar(BE + (c_e & 1)));
         }
         for (int u = 0; ok && u < n; ++u) {
-          const int st = u & 1, st1 = (u + 1) & 1;
+          const int f = c_f + u, st = f & 1, st1 = st ^ 1;
           const bool have_next = u + 1 < n;
-          if (!mbar_wait_fast(bar(BF + st), (u >> 1) & 1, cap, &abort_flag)) { ok = false; break; }
+          if (!mbar_wait_fast(bar(BF + st), (f >> 1) & 1, cap, &abort_flag)) { ok = false; break; }
           if (edge(u)) {
             mbar_arrive(bar(BY));
             if (!mbar_wait_fast(bar(BZ), z & 1, cap, &abort_flag)) { ok = false; break; }
             ++z;
           }
-          if (!mbar_wait_fast(bar(BP + 0), u & 1, cap, &abort_flag)) { ok = false; break; }
+          if (!mbar_wait_fast(bar(BP + 0), f & 1, cap, &abort_flag)) { ok = false; break; }
           tc_fence_after();
           issue_pv<D>(tO0, tS0, sV(st), u > 0);
           if (have_next) {
@@ -205,7 +241,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             umma_commit(bar(BS + 0));
           }
           if (two) {
-            if (!mbar_wait_fast(bar(BP + 1), u & 1, cap, &abort_flag)) { ok = false; break; }
+            if (!mbar_wait_fast(bar(BP + 1), (c_s1 + u) & 1, cap, &abort_flag)) { ok = false; break; }
             tc_fence_after();
             issue_pv<D>(tO1, tS1, sV(st), u > 0);
             if (have_next) {
@@ -213,35 +249,42 @@ __global__ void __launch_bounds__(kThreads, 1)
               umma_commit(bar(BS + 1));
             }
           }
-          umma_commit(bar(BE + st1));
+          umma_commit(bar(BE + ((c_e + u + 1) & 1)));
         }
         if (ok) umma_commit(bar(BO));
-        // every MMA issued must be finished before TMEM is released (bounded)
+        // every MMA issued must be finished before the tiles or TMEM are used again (bounded)
         umma_commit(bar(BDONE));
-        mbar_drain(bar(BDONE), 0, &abort_flag);
-      }
-    } else if (warp == 2) {
-      // ---------------------------------------------------------- value rows outside the unit's keys
-      int z = 0;
-      for (int j = 0; j < n; ++j) {
-        if (!edge(j)) continue;
-        // the MMA thread waits at this tile, so its stage's phase cannot move on
-        bool got = mbar_wait(bar(BY), z & 1, cap, &abort_flag);
-        got = got && mbar_wait(bar(BF + (j & 1)), (j >> 1) & 1, cap, &abort_flag);
-        if (__any_sync(0xffffffffu, !got)) break;
-        ++z;
-        const int k0 = (wk.t0 + j) * kTile;
-        for (int i = lane; i < kTile * 8; i += 32) {  // 16-byte chunk i % 8 of row i / 8 of each panel
-          const int key = k0 + (i >> 3);
-          if (key >= wk.lo && key < wk.hi) continue;
+        mbar_drain(bar(BDONE), c_piece & 1, &abort_flag);
+        c_z = z;
+      } else if (warp == 2 && n > 0) {
+        // -------------------------------------------------------- value rows outside the unit's keys
+        for (int j = 0; j < n; ++j) {
+          if (!edge(j)) continue;
+          // the MMA thread waits at this tile, so its stage's phase cannot move on
+          const int f = c_f + j;
+          bool got = mbar_wait(bar(BY), c_z & 1, cap, &abort_flag);
+          got = got && mbar_wait(bar(BF + (f & 1)), (f >> 1) & 1, cap, &abort_flag);
+          if (__any_sync(0xffffffffu, !got)) break;
+          ++c_z;
+          const int k0 = (wk.pc.t0 + j) * kTile;
+          for (int i = lane; i < kTile * 8; i += 32) {  // 16-byte chunk i % 8 of row i / 8 of each panel
+            const int key = k0 + (i >> 3);
+            if (key >= wk.pc.lo && key < wk.pc.hi) continue;
 #pragma unroll
-          for (int pn = 0; pn < C::kPanels; ++pn)
-            st_shared_v4(smem_u32(sV(j & 1)) + pn * 16384 + i * 16, 0u, 0u, 0u, 0u);
+            for (int pn = 0; pn < C::kPanels; ++pn)
+              st_shared_v4(smem_u32(sV(f & 1)) + pn * 16384 + i * 16, 0u, 0u, 0u, 0u);
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(bar(BZ));
         }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(BZ));
       }
+      __syncwarp();
+      count_piece(n);
+      meet();
+      if (*static_cast<volatile int*>(&abort_flag)) break;  // set before the barrier: the same for every thread
+      if (warp == 0) post_piece();
+      meet();
     }
   } else {
     // ============================================================ softmax warpgroups
@@ -249,160 +292,166 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int slot = (warp >> 2) - 1;
     const int quarter = warp & 3;
     const int row = quarter * 32 + lane;
-    const int r = wk.row0 + slot * kTile + row;  // row of the chunk: token r / G, head r % G
-    const bool valid = r < wk.rows;
-    const int q_len = wk.pc.sp.q_len, kv = wk.pc.sp.kv;
-    const int tok = valid ? r / p.G : 0;
-    const int h = wk.pc.hk * p.G + (valid ? r - tok * p.G : 0);
-    const int pos = kv - q_len + tok;
-    // keys [lo, hi) of this row; rows past the end see everything (their Q is 0, nothing of them is kept)
-    const int hi = valid ? min(kv, pos + 1) : 0x7fffffff;
-    const int lo = valid && p.window >= 0 ? max(0, pos - p.window + 1) : 0;
-    if (n > 0) {
-      // this thread's row of Q into the swizzled tile (K-major operand of S)
-      const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(wk.pc.sp.q0) + tok) * p.q_ss +
-                                                        static_cast<int64_t>(h) * p.q_sh);
-      const uint32_t dst = smem_u32(slot ? sQ1 : sQ0) + row * 128;
+    const uint32_t tS = tmem_addr(tmem + (slot ? C::kColS1 : C::kColS0), quarter * 32, 0);
+    const uint32_t tO = tmem_addr(tmem + (slot ? C::kColO1 : C::kColO0), quarter * 32, 0);
+    const uint32_t barS = bar(BS + slot), barP = bar(BP + slot);
+    while (wk.have) {
+      const int n = wk.n;
+      const int r = wk.row0 + slot * kTile + row;  // row of the chunk: token r / G, head r % G
+      const bool valid = r < wk.rows;
+      const int q_len = wk.pc.sp.q_len, kv = wk.pc.sp.kv;
+      const int tok = valid ? r / p.G : 0;
+      const int h = wk.pc.hk * p.G + (valid ? r - tok * p.G : 0);
+      const int pos = kv - q_len + tok;
+      // keys [lo, hi) of this row; rows past the end see everything (their Q is 0, nothing of them is kept)
+      const int hi = valid ? min(kv, pos + 1) : 0x7fffffff;
+      const int lo = valid && p.window >= 0 ? max(0, pos - p.window + 1) : 0;
+      if (n > 0) {
+        // this thread's row of Q into the swizzled tile (K-major operand of S)
+        const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(wk.pc.sp.q0) + tok) * p.q_ss +
+                                                          static_cast<int64_t>(h) * p.q_sh);
+        const uint32_t dst = smem_u32(slot ? sQ1 : sQ0) + row * 128;
 #pragma unroll
-      for (int c16 = 0; c16 < D / 8; ++c16) {
-        const uint4 v = valid ? src[c16] : make_uint4(0u, 0u, 0u, 0u);
-        st_shared_v4(dst + (c16 >> 3) * 16384 + (((c16 & 7) ^ (row & 7)) << 4), v.x, v.y, v.z, v.w);
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(BQ));
-    }
-    if (slot == 0 || wk.two) {
-      const uint32_t tS = tmem_addr(tmem + (slot ? C::kColS1 : C::kColS0), quarter * 32, 0);
-      const uint32_t tO = tmem_addr(tmem + (slot ? C::kColO1 : C::kColO0), quarter * 32, 0);
-      const uint32_t barS = bar(BS + slot), barP = bar(BP + slot);
-      const float c = kScore ? 1.f : p.scale_log2;
-      float slope = 0.f;
-      if constexpr (kScore) {
-        if (p.score.slopes) slope = __ldg(p.score.slopes + h) * kLog2e;
-      }
-      // keys that every row of the warp sees: tiles inside need no mask
-      const int all_lo = __reduce_max_sync(0xffffffffu, lo), all_hi = __reduce_min_sync(0xffffffffu, hi);
-      float m = -INFINITY, l = 0.f;
-      bool ok = true;
-      for (int t = 0; t < n; ++t) {
-        const int k0 = (wk.t0 + t) * kTile;
-        const bool got = mbar_wait(barS, t & 1, cap, &abort_flag);
-        if (__any_sync(0xffffffffu, !got)) { ok = false; break; }  // warp-uniform exit
-        tc_fence_after();
-        uint32_t sr[128];
-        tmem_ld_32x32b_x32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
-        tmem_ld_32x32b_x32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
-        tmem_ld_32x32b_x32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&sr[64]));
-        tmem_ld_32x32b_x32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&sr[96]));
-        tmem_wait_ld();
-        reg_fence(sr);
-        float* s = reinterpret_cast<float*>(sr);
-        if constexpr (kScore) shape_row(s, p.score, p.scale_log2, slope, pos - k0);
-        if (k0 < all_lo || k0 + kTile > all_hi) {
-          const int a = lo - k0, z = hi - k0;
-#pragma unroll
-          for (int j = 0; j < 128; ++j)
-            if (j < a || j >= z) s[j] = -INFINITY;
+        for (int c16 = 0; c16 < D / 8; ++c16) {
+          const uint4 v = valid ? src[c16] : make_uint4(0u, 0u, 0u, 0u);
+          st_shared_v4(dst + (c16 >> 3) * 16384 + (((c16 & 7) ^ (row & 7)) << 4), v.x, v.y, v.z, v.w);
         }
-        float mx8[8];
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(BQ));
+      }
+      if (slot == 0 || wk.two) {
+        const float c = kScore ? 1.f : p.scale_log2;
+        float slope = 0.f;
+        if constexpr (kScore) {
+          if (p.score.slopes) slope = __ldg(p.score.slopes + h) * kLog2e;
+        }
+        // keys that every row of the warp sees: tiles inside need no mask
+        const int all_lo = __reduce_max_sync(0xffffffffu, lo), all_hi = __reduce_min_sync(0xffffffffu, hi);
+        const int c_s = slot ? c_s1 : c_f;
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int t = 0; t < n; ++t) {
+          const int k0 = (wk.pc.t0 + t) * kTile;
+          const bool got = mbar_wait(barS, (c_s + t) & 1, cap, &abort_flag);
+          if (__any_sync(0xffffffffu, !got)) { ok = false; break; }  // warp-uniform exit
+          tc_fence_after();
+          uint32_t sr[128];
+          tmem_ld_32x32b_x32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&sr[0]));
+          tmem_ld_32x32b_x32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&sr[32]));
+          tmem_ld_32x32b_x32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&sr[64]));
+          tmem_ld_32x32b_x32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&sr[96]));
+          tmem_wait_ld();
+          reg_fence(sr);
+          float* s = reinterpret_cast<float*>(sr);
+          if constexpr (kScore) shape_row(s, p.score, p.scale_log2, slope, pos - k0);
+          if (k0 < all_lo || k0 + kTile > all_hi) {
+            const int a = lo - k0, z = hi - k0;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mx8[i] = s[i];
+            for (int j = 0; j < 128; ++j)
+              if (j < a || j >= z) s[j] = -INFINITY;
+          }
+          float mx8[8];
 #pragma unroll
-        for (int j = 8; j < 128; j += 2) mx8[(j >> 1) & 7] = fmax3(mx8[(j >> 1) & 7], s[j], s[j + 1]);
-        const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                               fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
-        const float mnew = fmaxf(m, mx * c);
-        // lazy rescale of O, decided by the whole warp (fwd.cu)
-        if (__any_sync(0xffffffffu, mnew > m + kRescaleThreshold)) {
-          const float alpha = (mnew == m) ? 1.f : ex2_approx(m - mnew);  // 0 when m = -inf
-          l *= alpha;
-          if (t > 0) {
+          for (int i = 0; i < 8; ++i) mx8[i] = s[i];
+#pragma unroll
+          for (int j = 8; j < 128; j += 2) mx8[(j >> 1) & 7] = fmax3(mx8[(j >> 1) & 7], s[j], s[j + 1]);
+          const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
+                                 fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+          const float mnew = fmaxf(m, mx * c);
+          // lazy rescale of O, decided by the whole warp (fwd.cu)
+          if (__any_sync(0xffffffffu, mnew > m + kRescaleThreshold)) {
+            const float alpha = (mnew == m) ? 1.f : ex2_approx(m - mnew);  // 0 when m = -inf
+            l *= alpha;
+            if (t > 0) {
 #pragma unroll 1
-            for (int cc = 0; cc < D / 32; ++cc) {
-              uint32_t o[32];
+              for (int cc = 0; cc < D / 32; ++cc) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(tO + cc * 32, o);
+                tmem_wait_ld();
+                reg_fence(o);
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
+                tmem_st_32x32b_x32(tO + cc * 32, o);
+              }
+            }
+            m = mnew;
+          }
+          const float mref = (m == -INFINITY) ? 0.f : m;
+          uint64_t rs2[4] = {0, 0, 0, 0};
+          const uint64_t c2 = f2_pack(c, c), nm2 = f2_pack(-mref, -mref);
+          uint32_t pk[64];
+#pragma unroll
+          for (int j = 0; j < 64; ++j) {
+            const uint64_t x2 = f2_fma(f2_pack(s[2 * j], s[2 * j + 1]), c2, nm2);
+            float x0, x1;
+            f2_unpack(x2, x0, x1);
+            const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+            rs2[j & 3] = f2_add(rs2[j & 3], f2_pack(p0, p1));
+            pk[j] = pack_bf16x2(p0, p1);
+          }
+          float rr[8];
+          f2_unpack(f2_add(rs2[0], rs2[1]), rr[0], rr[1]);
+          f2_unpack(f2_add(rs2[2], rs2[3]), rr[2], rr[3]);
+          l += (rr[0] + rr[2]) + (rr[1] + rr[3]);
+          tmem_st_32x32b_x32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
+          tmem_st_32x32b_x32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
+          tmem_wait_st();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(barP);
+        }
+        // -------------------------------------------------------- epilogue
+        if (ok && n > 0) {
+          const bool got = mbar_wait(bar(BO), c_piece & 1, cap, &abort_flag);
+          ok = !__any_sync(0xffffffffu, !got);
+        }
+        tc_fence_after();
+        if (ok) {
+          const bool whole = wk.pc.whole != 0;
+          const float inv = l > 0.f ? 1.f / l : 0.f;
+          const int64_t gtok = static_cast<int64_t>(wk.pc.sp.q0) + tok;
+          const int64_t wr = static_cast<int64_t>(wk.pc.place) * kUnitRows + slot * kTile + row;
+          __nv_bfloat16* op = p.out + gtok * p.o_ss + static_cast<int64_t>(h) * p.o_sh;
+#pragma unroll 1
+          for (int cc = 0; cc < D / 32; ++cc) {
+            uint32_t o[32];
+            if (n > 0) {
               tmem_ld_32x32b_x32(tO + cc * 32, o);
               tmem_wait_ld();
               reg_fence(o);
+            } else {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * alpha);
-              tmem_st_32x32b_x32(tO + cc * 32, o);
+              for (int j = 0; j < 32; ++j) o[j] = 0u;
+            }
+            if (valid && whole) {
+#pragma unroll
+              for (int j = 0; j < 4; ++j) {
+                uint32_t w[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  w[e] = pack_bf16x2(__uint_as_float(o[8 * j + 2 * e]) * inv, __uint_as_float(o[8 * j + 2 * e + 1]) * inv);
+                reinterpret_cast<uint4*>(op + cc * 32)[j] = make_uint4(w[0], w[1], w[2], w[3]);
+              }
+            } else if (valid) {
+              uint4* d4 = reinterpret_cast<uint4*>(p.ws_o + wr * D + cc * 32);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) d4[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
             }
           }
-          m = mnew;
-        }
-        const float mref = (m == -INFINITY) ? 0.f : m;
-        uint64_t rs2[4] = {0, 0, 0, 0};
-        const uint64_t c2 = f2_pack(c, c), nm2 = f2_pack(-mref, -mref);
-        uint32_t pk[64];
-#pragma unroll
-        for (int j = 0; j < 64; ++j) {
-          const uint64_t x2 = f2_fma(f2_pack(s[2 * j], s[2 * j + 1]), c2, nm2);
-          float x0, x1;
-          f2_unpack(x2, x0, x1);
-          const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-          rs2[j & 3] = f2_add(rs2[j & 3], f2_pack(p0, p1));
-          pk[j] = pack_bf16x2(p0, p1);
-        }
-        float rr[8];
-        f2_unpack(f2_add(rs2[0], rs2[1]), rr[0], rr[1]);
-        f2_unpack(f2_add(rs2[2], rs2[3]), rr[2], rr[3]);
-        l += (rr[0] + rr[2]) + (rr[1] + rr[3]);
-        tmem_st_32x32b_x32(tS + 0, *reinterpret_cast<uint32_t(*)[32]>(&pk[0]));
-        tmem_st_32x32b_x32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&pk[32]));
-        tmem_wait_st();
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(barP);
-      }
-      // ---------------------------------------------------------- epilogue
-      if (ok && n > 0) {
-        const bool got = mbar_wait(bar(BO), 0, cap, &abort_flag);
-        ok = !__any_sync(0xffffffffu, !got);
-      }
-      tc_fence_after();
-      if (ok) {
-        const bool whole = wk.pc.nseg == 1;
-        const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
-        const int64_t gtok = static_cast<int64_t>(wk.pc.sp.q0) + tok;
-        const int64_t seg = wk.pc.seg0 + static_cast<int64_t>(wk.pc.i) * wk.pc.sp.rts;
-        const int64_t wr = seg * kUnitRows + slot * kTile + row;
-        const bool store = valid && (whole || seg < p.max_segs);
-        __nv_bfloat16* op = p.out + gtok * p.o_ss + static_cast<int64_t>(h) * p.o_sh;
-#pragma unroll 1
-        for (int cc = 0; cc < D / 32; ++cc) {
-          uint32_t o[32];
-          if (n > 0) {
-            tmem_ld_32x32b_x32(tO + cc * 32, o);
-            tmem_wait_ld();
-            reg_fence(o);
-          } else {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = 0u;
-          }
-          if (store && whole) {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                w[e] = pack_bf16x2(__uint_as_float(o[8 * j + 2 * e]) * inv, __uint_as_float(o[8 * j + 2 * e + 1]) * inv);
-              reinterpret_cast<uint4*>(op + cc * 32)[j] = make_uint4(w[0], w[1], w[2], w[3]);
-            }
-          } else if (store) {
-            uint4* d4 = reinterpret_cast<uint4*>(p.ws_o + wr * D + cc * 32);
-#pragma unroll
-            for (int j = 0; j < 8; ++j) d4[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+          if (valid && whole) {
+            if (p.lse)
+              p.lse[static_cast<int64_t>(h) * p.total_q + gtok] =
+                  l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+          } else if (valid) {
+            p.ws_ml[wr] = make_float2(m, l);
           }
         }
-        if (store && whole) {
-          if (p.lse)
-            p.lse[static_cast<int64_t>(h) * p.total_q + gtok] =
-                l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
-        } else if (store) {
-          p.ws_ml[wr] = make_float2(m, l);
-        }
       }
+      count_piece(n);
+      meet();
+      if (*static_cast<volatile int*>(&abort_flag)) break;
+      meet();
     }
   }
 
@@ -432,17 +481,14 @@ static cudaError_t launch_tiles_one(const CUtensorMap& tk, const CUtensorMap& tv
                                 Cfg<D>::kSmemBytes);
   });
   if (ready != cudaSuccess) return ready;
-  k_chunk_tiles<D, kScore><<<p.max_segs, kThreads, Cfg<D>::kSmemBytes, s>>>(tk, tv, p);
+  k_chunk_tiles<D, kScore><<<p.slots, kThreads, Cfg<D>::kSmemBytes, s>>>(tk, tv, p);
   return cudaGetLastError();
 }
 
 cudaError_t launch_chunk_tiles(const CUtensorMap& tk, const CUtensorMap& tv, const ChunkParams& p, cudaStream_t s) {
-  if (p.max_segs <= 0 || p.max_units <= 0) return cudaSuccess;
   const bool shaped = p.score.c1 != 0.f || p.score.slopes;
-  cudaError_t e;
-  if (p.D == 64) e = shaped ? launch_tiles_one<64, true>(tk, tv, p, s) : launch_tiles_one<64, false>(tk, tv, p, s);
-  else e = shaped ? launch_tiles_one<128, true>(tk, tv, p, s) : launch_tiles_one<128, false>(tk, tv, p, s);
-  return e != cudaSuccess ? e : launch_chunk_join(p, kUnitRows, kTile, s);
+  if (p.D == 64) return shaped ? launch_tiles_one<64, true>(tk, tv, p, s) : launch_tiles_one<64, false>(tk, tv, p, s);
+  return shaped ? launch_tiles_one<128, true>(tk, tv, p, s) : launch_tiles_one<128, false>(tk, tv, p, s);
 }
 
 }  // namespace bfa

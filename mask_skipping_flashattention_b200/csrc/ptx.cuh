@@ -346,6 +346,13 @@ __device__ __forceinline__ void umma_commit(uint32_t bar) {
       : "memory");
 }
 
+// ---------------------------------------------------------------- dependent launches
+// A kernel launched as a programmatic dependent may start once every block of the
+// kernel before it has called grid_trigger (or exited); grid_wait holds it until
+// that kernel is complete and its writes are visible.
+__device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // ---------------------------------------------------------------- registers
 // Move per-thread registers between warpgroups (all 4 warps of a warpgroup
 // execute the same instruction).  The sum over the block after the moves must
