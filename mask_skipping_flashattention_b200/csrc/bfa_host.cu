@@ -1001,10 +1001,27 @@ int sm_count() {
 
 // cap and penalty of a call with softmax scale `scale` (softcap 0: none)
 ScoreParams score_params(float scale, float softcap, const float* slopes) {
+  static const double kTerms[kTanhTerms] = {0.99999995,   -0.333328392,   0.133252041,  -0.0534570294,
+                                            0.0202899801, -0.00620337882, 0.00104102254};
   ScoreParams sp;
-  sp.c0 = softcap > 0.f ? scale / softcap : 0.f;
-  sp.c1 = softcap > 0.f ? softcap * kLog2e : 0.f;
+  std::memset(&sp, 0, sizeof(sp));
   sp.slopes = slopes;
+  sp.poly_max = -1.f;
+  if (!(softcap > 0.f)) return sp;
+  const double c0 = static_cast<double>(scale) / softcap, c1 = static_cast<double>(softcap) * 1.4426950408889634;
+  sp.c0 = static_cast<float>(c0);
+  sp.c1 = static_cast<float>(c1);
+  sp.ninv_c1_sq = static_cast<float>(-1.0 / (c1 * c1));
+  // The folded polynomial serves |x| <= 1; where a small c0 (a large cap) pushes its last
+  // coefficients below what fp32 holds well, only as far as their terms do not count.
+  double x_max = 1.0, most = 0.0;
+  for (int k = 0; k < kTanhTerms; ++k) {
+    const double v = kTerms[k] * c1 * std::pow(c0, 2 * k + 1);
+    sp.poly[k] = static_cast<float>(v);
+    most = std::max(most, std::fabs(v));
+    if (std::fabs(v) < 1e-38) x_max = std::min(x_max, k == 0 ? 0.0 : std::pow(1e-8 / std::fabs(kTerms[k]), 0.5 / k));
+  }
+  if (x_max > 0 && sp.c0 > 0.f && most < 1e30) sp.poly_max = static_cast<float>(std::min(x_max / c0, 1e15));
   return sp;
 }
 
@@ -1248,6 +1265,11 @@ bfa_status bwd_launch_from_host(bfa_plan* P, const void* q, const void* k, const
   // heads, measured faster.
   const bool fused_order = D == 128 && !g_bwd_deterministic && !P->varlen;
   p.kv_chunk = fused_order ? 1 : static_cast<int>(chunk_for(n_cols, p.rep_kv));
+  // Shaped calls with few columns in all take them longest first over every replica,
+  // so that no long column starts late (measured: 256 columns of a causal 8192 row 1583 ->
+  // 1150 us, 512 of 4 x 4096 tokens 1347 -> 1234 us).
+  if ((softcap != 0.f || slopes) && fused_order && static_cast<int64_t>(n_cols) * p.rep_kv <= 8LL * sm_count())
+    p.kv_chunk = p.rep_kv;
   p.varlen = P->varlen;
   p.Sq_lse = P->sq;
   const float sc = (scale > 0.f) ? scale : 1.0f / std::sqrt(static_cast<float>(D));

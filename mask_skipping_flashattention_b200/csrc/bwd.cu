@@ -276,7 +276,7 @@ struct DqWork {
 // the previous tile's dQ products may still read.
 constexpr int kDqThreads = 384;
 
-template <int D, bool kScore>
+template <int D, int kScore>
 __global__ void __launch_bounds__(kDqThreads, 1)
     k_bwd_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
              const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const BwdParams p) {
@@ -436,9 +436,8 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     const float nlse2 = p.ws_lse2[wi], nd = p.ws_d[wi];  // -LSE * log2(e), -D
     const float c = p.scale_log2;
     float slope = 0.f;
-    if constexpr (kScore) {
-      if (p.score.slopes) slope = __ldg(p.score.slopes + wk.h) * kLog2e;
-    }
+    if constexpr ((kScore & kScoreSlopes) != 0) slope = __ldg(p.score.slopes + wk.h) * kLog2e;
+    (void)slope;
     bool ok = true;
     int kt_next = n > 0 ? p.plan.kv_tile[wk.e0] : 0;
     int part_next = n > 0 ? p.plan.part[wk.e0] : -1;
@@ -470,25 +469,27 @@ __global__ void __launch_bounds__(kDqThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(BC));
       const uint32_t tdS = tLane + 384 + 64 * (u & 1);
-      ScoreBias bias;
-      if constexpr (kScore) bias = score_bias(slope, qpos - kt * kTile, -1);
+      ScoreBias bias = {};
+      bias.linear = true;
+      if constexpr ((kScore & kScoreSlopes) != 0) bias = score_bias(slope, qpos - kt * kTile, -1);
 #pragma unroll
       for (int cc = 0; cc < 2; ++cc) {
         const int gc = 2 * half + cc;  // 32-key chunk of the tile
         uint32_t pk[16];
-        if constexpr (kScore) {
+        if constexpr (kScore != 0) {
           const uint32_t bits = half ? am[2 + cc] : am[cc];
-          score_dispatch(score_form(sv[cc], p.score), masked || !bias.linear, [&](auto form, auto slow) {
+          score_dispatch<kScore>(sv[cc], p.score, masked || !bias.linear, [&](auto form, auto slow) {
 #pragma unroll
             for (int jj = 0; jj < 16; ++jj) {
               const int c0 = 2 * jj;
-              uint64_t z, f, w;
-              shape_pair<form.value, slow.value>(__uint_as_float(sv[cc][c0]), __uint_as_float(sv[cc][c0 + 1]),
-                                                 64 * half + 32 * cc + c0, c0, bits, bias, p.score, c, z, f);
-              float z0, z1, d0, d1;
-              f2_unpack(f2_add(z, f2_pack(nlse2, nlse2)), z0, z1);
-              w = f2_pack(ex2_approx(z0), ex2_approx(z1));
-              if (form.value != kTanhNone) w = f2_mul(w, f);
+              uint64_t x, f, w;
+              shape_pair<kScore, form.value, slow.value>(
+                  __uint_as_float(sv[cc][c0]), __uint_as_float(sv[cc][c0 + 1]), 64 * half + 32 * cc + c0, c0, bits, bias,
+                  p.score, c, f2_pack(nlse2, nlse2), x, f);
+              float x0, x1, d0, d1;
+              f2_unpack(x, x0, x1);
+              w = f2_pack(ex2_approx(x0), ex2_approx(x1));
+              if (kScore & kScoreCap) w = f2_mul(w, f);
               f2_unpack(f2_mul(w, f2_add(f2_pack(__uint_as_float(dv[cc][c0]), __uint_as_float(dv[cc][c0 + 1])),
                                          f2_pack(nd, nd))),
                         d0, d1);
@@ -554,7 +555,7 @@ struct KvWork {
   int32_t kt, e0, nq, nh, b, hk, steps;
 };
 
-template <int D, bool kScore>
+template <int D, int kScore>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     k_bwd_dkdv(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO, const BwdParams p) {
@@ -736,11 +737,10 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (__any_sync(0xffffffffu, !gs)) { ok = false; break; }
       tc_fence_after();
       const uint32_t sLse = smem_u32(sVec(st)), sDv = smem_u32(sVec(st) + kTile);
-      ScoreBias bias;
-      if constexpr (kScore) {
-        const float slope = p.score.slopes ? __ldg(p.score.slopes + step_head(s)) * kLog2e : 0.f;
-        bias = score_bias(slope, qt * kTile - kpos, 1);
-      }
+      ScoreBias bias = {};
+      bias.linear = true;
+      if constexpr ((kScore & kScoreSlopes) != 0)
+        bias = score_bias(__ldg(p.score.slopes + step_head(s)) * kLog2e, qt * kTile - kpos, 1);
       // phase 1: P^T = 2^(scale log2(e) S^T - LSE log2(e)) for the 128 queries, kept
       // in fp32 for phase 2 and written as bf16 over S^T (chunks of 32 queries,
       // the next chunk's load in flight; a chunk's P^T columns lie in columns
@@ -762,22 +762,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
               if (!((bits >> j) & 1u)) sv[j] = __float_as_uint(-INFINITY);
           }
           uint32_t pkp[16];
-          if constexpr (kScore) {
-            score_dispatch(score_form(sv, p.score), masked || !bias.linear, [&](auto form, auto slow) {
+          if constexpr (kScore != 0) {
+            score_dispatch<kScore>(sv, p.score, masked || !bias.linear, [&](auto form, auto slow) {
 #pragma unroll
               for (int q4 = 0; q4 < 8; ++q4) {
                 const float4 L = ld_shared_f4(sLse + (cc * 32 + q4 * 4) * 4);
 #pragma unroll
                 for (int h2 = 0; h2 < 2; ++h2) {
                   const int col = q4 * 4 + 2 * h2;
-                  uint64_t z, f;
-                  shape_pair<form.value, slow.value>(__uint_as_float(sv[col]), __uint_as_float(sv[col + 1]),
-                                                     cc * 32 + col, col, am[cc], bias, p.score, c, z, f);
+                  uint64_t x, f;
+                  shape_pair<kScore, form.value, slow.value>(
+                      __uint_as_float(sv[col]), __uint_as_float(sv[col + 1]), cc * 32 + col, col, am[cc], bias, p.score, c,
+                      h2 ? f2_pack(L.z, L.w) : f2_pack(L.x, L.y), x, f);
                   float x0, x1;
-                  f2_unpack(f2_add(z, h2 ? f2_pack(L.z, L.w) : f2_pack(L.x, L.y)), x0, x1);
+                  f2_unpack(x, x0, x1);
                   const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
                   // phase 2 needs P only with the cap's factor
-                  pv[cc * 16 + 2 * q4 + h2] = form.value != kTanhNone ? f2_mul(f2_pack(p0, p1), f) : f2_pack(p0, p1);
+                  pv[cc * 16 + 2 * q4 + h2] =
+                      (kScore & kScoreCap) ? f2_mul(f2_pack(p0, p1), f) : f2_pack(p0, p1);
                   pkp[2 * q4 + h2] = pack_bf16x2(p0, p1);
                 }
               }
@@ -913,7 +915,7 @@ struct FCfg {
 };
 static_assert(FCfg::kSmemBytes <= 232448, "fused pass shared memory");
 
-template <bool kScore>
+template <int kScore>
 __global__ void __launch_bounds__(kFusedThreads, 1)
     k_bwd_fused(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                 const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO, const BwdParams p) {
@@ -1121,11 +1123,10 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
       if (__any_sync(0xffffffffu, !gs)) { ok = false; break; }
       tc_fence_after();
       const uint32_t sLse = smem_u32(sVec(st)), sDv = smem_u32(sVec(st) + kTile);
-      ScoreBias bias;
-      if constexpr (kScore) {
-        const float slope = p.score.slopes ? __ldg(p.score.slopes + step_head(s)) * kLog2e : 0.f;
-        bias = score_bias(slope, qt * kTile - kpos, 1);
-      }
+      ScoreBias bias = {};
+      bias.linear = true;
+      if constexpr ((kScore & kScoreSlopes) != 0)
+        bias = score_bias(__ldg(p.score.slopes + step_head(s)) * kLog2e, qt * kTile - kpos, 1);
       // phase 1: P^T = 2^(scale log2(e) S^T - LSE log2(e)), kept in fp32 for
       // phase 2 and written as bf16 over S^T, 32 queries at a time
       uint64_t pv[64];
@@ -1145,22 +1146,24 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
               if (!((bits >> j) & 1u)) sv[j] = __float_as_uint(-INFINITY);
           }
           uint32_t pkp[16];
-          if constexpr (kScore) {
-            score_dispatch(score_form(sv, p.score), masked || !bias.linear, [&](auto form, auto slow) {
+          if constexpr (kScore != 0) {
+            score_dispatch<kScore>(sv, p.score, masked || !bias.linear, [&](auto form, auto slow) {
 #pragma unroll
               for (int q4 = 0; q4 < 8; ++q4) {
                 const float4 L = ld_shared_f4(sLse + (cc * 32 + q4 * 4) * 4);
 #pragma unroll
                 for (int h2 = 0; h2 < 2; ++h2) {
                   const int col = q4 * 4 + 2 * h2;
-                  uint64_t z, f;
-                  shape_pair<form.value, slow.value>(__uint_as_float(sv[col]), __uint_as_float(sv[col + 1]),
-                                                     cc * 32 + col, col, am[cc], bias, p.score, c, z, f);
+                  uint64_t x, f;
+                  shape_pair<kScore, form.value, slow.value>(
+                      __uint_as_float(sv[col]), __uint_as_float(sv[col + 1]), cc * 32 + col, col, am[cc], bias, p.score, c,
+                      h2 ? f2_pack(L.z, L.w) : f2_pack(L.x, L.y), x, f);
                   float x0, x1;
-                  f2_unpack(f2_add(z, h2 ? f2_pack(L.z, L.w) : f2_pack(L.x, L.y)), x0, x1);
+                  f2_unpack(x, x0, x1);
                   const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
                   // phase 2 needs P only with the cap's factor
-                  pv[cc * 16 + 2 * q4 + h2] = form.value != kTanhNone ? f2_mul(f2_pack(p0, p1), f) : f2_pack(p0, p1);
+                  pv[cc * 16 + 2 * q4 + h2] =
+                      (kScore & kScoreCap) ? f2_mul(f2_pack(p0, p1), f) : f2_pack(p0, p1);
                   pkp[2 * q4 + h2] = pack_bf16x2(p0, p1);
                 }
               }
@@ -1362,9 +1365,7 @@ static cudaError_t bwd_prepare(K kernel, int smem) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 
-static bool shaped(const BwdParams& p) { return p.score.c1 != 0.f || p.score.slopes != nullptr; }
-
-template <int D, bool kScore>
+template <int D, int kScore>
 static cudaError_t launch_dq_as(const CUtensorMap& tq, const CUtensorMap& tdo, const CUtensorMap& tk,
                                 const CUtensorMap& tv, const BwdParams& p, int64_t n_work, cudaStream_t s) {
   static DeviceOnce once;
@@ -1377,11 +1378,12 @@ static cudaError_t launch_dq_as(const CUtensorMap& tq, const CUtensorMap& tdo, c
 template <int D>
 static cudaError_t launch_dq_one(const CUtensorMap& tq, const CUtensorMap& tdo, const CUtensorMap& tk,
                                  const CUtensorMap& tv, const BwdParams& p, int64_t n_work, cudaStream_t s) {
-  return shaped(p) ? launch_dq_as<D, true>(tq, tdo, tk, tv, p, n_work, s)
-                   : launch_dq_as<D, false>(tq, tdo, tk, tv, p, n_work, s);
+  return for_score_mode(p.score.mode(), [&](auto mode) {
+    return launch_dq_as<D, decltype(mode)::value>(tq, tdo, tk, tv, p, n_work, s);
+  });
 }
 
-template <int D, bool kScore>
+template <int D, int kScore>
 static cudaError_t launch_dkdv_as(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                                   const CUtensorMap& tdo, const BwdParams& p, int64_t n_work, cudaStream_t s) {
   static DeviceOnce once;
@@ -1394,8 +1396,9 @@ static cudaError_t launch_dkdv_as(const CUtensorMap& tk, const CUtensorMap& tv, 
 template <int D>
 static cudaError_t launch_dkdv_one(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                                    const CUtensorMap& tdo, const BwdParams& p, int64_t n_work, cudaStream_t s) {
-  return shaped(p) ? launch_dkdv_as<D, true>(tk, tv, tq, tdo, p, n_work, s)
-                   : launch_dkdv_as<D, false>(tk, tv, tq, tdo, p, n_work, s);
+  return for_score_mode(p.score.mode(), [&](auto mode) {
+    return launch_dkdv_as<D, decltype(mode)::value>(tk, tv, tq, tdo, p, n_work, s);
+  });
 }
 
 cudaError_t launch_bwd_dq(int D, const CUtensorMap& tq, const CUtensorMap& tdo, const CUtensorMap& tk,
@@ -1405,7 +1408,7 @@ cudaError_t launch_bwd_dq(int D, const CUtensorMap& tq, const CUtensorMap& tdo, 
   return D == 64 ? launch_dq_one<64>(tq, tdo, tk, tv, p, n_work, s) : launch_dq_one<128>(tq, tdo, tk, tv, p, n_work, s);
 }
 
-template <bool kScore>
+template <int kScore>
 static cudaError_t launch_fused_as(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                                    const CUtensorMap& tdo, const BwdParams& p, int64_t n_work, cudaStream_t s) {
   // the setmaxnreg split is only safe with exactly kFusedRegsLaunch registers a thread
@@ -1426,8 +1429,9 @@ cudaError_t launch_bwd_fused(const CUtensorMap& tk, const CUtensorMap& tv, const
                              const CUtensorMap& tdo, const BwdParams& p, int64_t n_work, cudaStream_t s) {
   if (n_work <= 0) return cudaSuccess;
   if (n_work > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return shaped(p) ? launch_fused_as<true>(tk, tv, tq, tdo, p, n_work, s)
-                   : launch_fused_as<false>(tk, tv, tq, tdo, p, n_work, s);
+  return for_score_mode(p.score.mode(), [&](auto mode) {
+    return launch_fused_as<decltype(mode)::value>(tk, tv, tq, tdo, p, n_work, s);
+  });
 }
 
 cudaError_t launch_bwd_dq_store(const BwdParams& p, cudaStream_t s) {

@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) k_chunk_rows(const ChunkParams
           const int i = e >> 1, key = kb + j * 8 + (lane & 3) * 2 + (e & 1);
           float z = s[j][e];
           if constexpr (kScore) {
-            z = p.score.c1 != 0.f ? p.score.c1 * tanh_any(z * p.score.c0) : z * p.scale_log2;
+            z = p.score.c1 != 0.f ? capped_any(z, p.score) : z * p.scale_log2;
             z = fmaf(-slope[i], static_cast<float>(pos[i] - key), z);
           } else {
             z *= p.scale_log2;
@@ -496,7 +496,7 @@ static cudaError_t launch_rows_one(const ChunkParams& p, bool after_tiles, cudaS
 }
 
 cudaError_t launch_chunk_rows(const ChunkParams& p, bool after_tiles, cudaStream_t s) {
-  const bool shaped = p.score.c1 != 0.f || p.score.slopes;
+  const bool shaped = p.score.mode() != kScorePlain;
   if (p.D == 64) return shaped ? launch_rows_one<64, true>(p, after_tiles, s) : launch_rows_one<64, false>(p, after_tiles, s);
   return shaped ? launch_rows_one<128, true>(p, after_tiles, s) : launch_rows_one<128, false>(p, after_tiles, s);
 }

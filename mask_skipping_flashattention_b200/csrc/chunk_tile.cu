@@ -49,7 +49,7 @@ struct TileWork {
 
 }  // namespace
 
-template <int D, bool kScore>
+template <int D, int kScore>
 __global__ void __launch_bounds__(kThreads, 1)
     k_chunk_tiles(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                   const ChunkParams p) {
@@ -323,9 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (slot == 0 || wk.two) {
         const float c = kScore ? 1.f : p.scale_log2;
         float slope = 0.f;
-        if constexpr (kScore) {
-          if (p.score.slopes) slope = __ldg(p.score.slopes + h) * kLog2e;
-        }
+        if constexpr ((kScore & kScoreSlopes) != 0) slope = __ldg(p.score.slopes + h) * kLog2e;
         // keys that every row of the warp sees: tiles inside need no mask
         const int all_lo = __reduce_max_sync(0xffffffffu, lo), all_hi = __reduce_min_sync(0xffffffffu, hi);
         const int c_s = slot ? c_s1 : c_f;
@@ -344,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld();
           reg_fence(sr);
           float* s = reinterpret_cast<float*>(sr);
-          if constexpr (kScore) shape_row(s, p.score, p.scale_log2, slope, pos - k0);
+          if constexpr (kScore != 0) shape_row<kScore>(s, p.score, p.scale_log2, slope, pos - k0);
           if (k0 < all_lo || k0 + kTile > all_hi) {
             const int a = lo - k0, z = hi - k0;
 #pragma unroll
@@ -468,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // ----------------------------------------------------------------------------
 // launcher (host)
 // ----------------------------------------------------------------------------
-template <int D, bool kScore>
+template <int D, int kScore>
 static cudaError_t launch_tiles_one(const CUtensorMap& tk, const CUtensorMap& tv, const ChunkParams& p, cudaStream_t s) {
   static DeviceOnce once;
   const cudaError_t ready = once.run([] {
@@ -486,9 +484,10 @@ static cudaError_t launch_tiles_one(const CUtensorMap& tk, const CUtensorMap& tv
 }
 
 cudaError_t launch_chunk_tiles(const CUtensorMap& tk, const CUtensorMap& tv, const ChunkParams& p, cudaStream_t s) {
-  const bool shaped = p.score.c1 != 0.f || p.score.slopes;
-  if (p.D == 64) return shaped ? launch_tiles_one<64, true>(tk, tv, p, s) : launch_tiles_one<64, false>(tk, tv, p, s);
-  return shaped ? launch_tiles_one<128, true>(tk, tv, p, s) : launch_tiles_one<128, false>(tk, tv, p, s);
+  return for_score_mode(p.score.mode(), [&](auto mode) {
+    constexpr int kMode = decltype(mode)::value;
+    return p.D == 64 ? launch_tiles_one<64, kMode>(tk, tv, p, s) : launch_tiles_one<128, kMode>(tk, tv, p, s);
+  });
 }
 
 }  // namespace bfa

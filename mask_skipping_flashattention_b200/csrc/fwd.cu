@@ -226,7 +226,7 @@ __device__ __forceinline__ bool tile_skipped(const int (&votes)[2][4], int t) {
 // boxes, rows mapped to (position, head)); kScore: shaped scores (score.cuh), which
 // the softmax warps make of S right after they load it, so that the rest of the
 // loop is the plain kernel's with a scale of 1; the other kernels hold none of it.
-template <int D, bool kSkip, bool kPacked, bool kScore>
+template <int D, bool kSkip, bool kPacked, int kScore>
 __global__ void __launch_bounds__(kThreads, 1)
     bfa_fwd_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmK,
                    const __grid_constant__ CUtensorMap tmV, const __grid_constant__ CUtensorMap tmO,
@@ -413,9 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int qpos = (slot ? wk.qt[1] : wk.qt[0]) * kTile + row;  // position of this row inside its group
       const float c = kScore ? 1.f : p.scale_log2;
       float slope = 0.f;
-      if constexpr (kScore) {
-        if (p.score.slopes) slope = __ldg(p.score.slopes + (slot ? wk.h[1] : wk.h[0])) * kLog2e;
-      }
+      if constexpr ((kScore & kScoreSlopes) != 0) slope = __ldg(p.score.slopes + (slot ? wk.h[1] : wk.h[0])) * kLog2e;
       float m = -INFINITY, l = 0.f;
       bool ok = true;
       int kt_next = n > 0 ? p.plan.kv_tile[e0] : 0;
@@ -448,7 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
         reg_fence(sr);
         float* s = reinterpret_cast<float*>(sr);
-        if constexpr (kScore) shape_row(s, p.score, p.scale_log2, slope, qpos - kt * kTile);
+        if constexpr (kScore != 0) shape_row<kScore>(s, p.score, p.scale_log2, slope, qpos - kt * kTile);
         if (masked) {
 #pragma unroll
           for (int j = 0; j < 128; ++j)
@@ -666,7 +664,7 @@ static cudaError_t prepare(K kernel, int smem) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 
-template <int D, bool kSkip, bool kPacked, bool kScore = false>
+template <int D, bool kSkip, bool kPacked, int kScore = kScorePlain>
 static cudaError_t launch_one(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                               const CUtensorMap& to, const FwdParams& p, int64_t n_work, cudaStream_t s) {
   static DeviceOnce once;
@@ -682,9 +680,11 @@ template <int D>
 static cudaError_t launch_d(const CUtensorMap& tq, const CUtensorMap& tk, const CUtensorMap& tv,
                             const CUtensorMap& to, const FwdParams& p, int64_t n_work, cudaStream_t s) {
   const bool approx = p.skip_log2 > 0.f, packed = p.pack_g > 1;
-  if (p.score.c1 != 0.f || p.score.slopes) {  // the host refuses these with packed plans or skipping
+  if (p.score.mode() != kScorePlain) {  // the host refuses these with packed plans or skipping
     if (packed || approx) return cudaErrorInvalidValue;
-    return launch_one<D, false, false, true>(tq, tk, tv, to, p, n_work, s);
+    return for_score_mode(p.score.mode(), [&](auto mode) {
+      return launch_one<D, false, false, decltype(mode)::value>(tq, tk, tv, to, p, n_work, s);
+    });
   }
   if (packed)
     return approx ? launch_one<D, true, true>(tq, tk, tv, to, p, n_work, s)
@@ -707,14 +707,14 @@ cudaError_t launch_wait_selftest(uint32_t* err, uint64_t cap, cudaStream_t s) {
 
 cudaError_t probe_fwd_kernels() {
   cudaFuncAttributes a;
-  cudaError_t e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<128, false, false, false>);
-  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<64, false, false, false>);
-  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<128, true, false, false>);
-  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<64, true, false, false>);
-  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<128, false, true, false>);
-  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<64, false, true, false>);
-  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<128, false, false, true>);
-  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<64, false, false, true>);
+  cudaError_t e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<128, false, false, kScorePlain>);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<64, false, false, kScorePlain>);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<128, true, false, kScorePlain>);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<64, true, false, kScorePlain>);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<128, false, true, kScorePlain>);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<64, false, true, kScorePlain>);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<128, false, false, kScoreCapSlopes>);
+  if (e == cudaSuccess) e = cudaFuncGetAttributes(&a, bfa_fwd_kernel<64, false, false, kScoreCapSlopes>);
   return e;
 }
 

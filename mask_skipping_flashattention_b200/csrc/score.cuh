@@ -3,12 +3,19 @@
 // carried in log2 units (times log2 e), and the factor 1 - tanh^2 that the
 // cap's chain rule puts on the score gradient.
 //
-// tanh: |x| <= kTanhPoly takes the odd polynomial x * P(x^2) (a minimax fit of
-// tanh(x) / x, relative error 3e-8, 1.6e-7 as evaluated in fp32); larger |x| take
-// 1 - 2 / (1 + e^(2|x|)), whose absolute error of about 2e-7 is a relative one
-// of 4e-7 there.  Both keep the score's error proportional to the score, which
-// the hardware's tanh (relative 2^-11) would not: with a cap of 50 that one moves a
-// score by up to 0.02 and its weight by 2 %.
+// tanh(x), x = c0 s with c0 = scale / cap, from minimax fits of tanh(x) / x in u = x^2:
+//   |x| <= 1  7 terms, relative error 5e-8 (1.6e-7 as evaluated in fp32);
+//   any x     5 terms over 5, to |x| = 9 (then constant), 2e-8 (3.3e-7).
+// They keep the score's error proportional to the score, which the hardware's tanh
+// (relative 2^-11) would not: with a cap of 50 that one moves a score by up to 0.02 and
+// its weight by 2 %.  In the first, scale, cap and log2 e are folded into the
+// coefficients, so that a score costs its square, the terms and one product: the
+// softmax warps are bound by the instructions they issue (about 3 a score without a
+// shape; 7 and 12 with these).  Which form a group of scores takes is decided by its
+// largest magnitude, a warp at a time.  More forms were slower: with 5 folded terms to
+// 0.625 and 8 to 1 beside the last, a backward that stays in the 8-term form takes 1628 us
+// (4 x 4096 tokens, 16 / 4 heads, D 128), with the 8-term and the last form alone 1264 us: the
+// kernel's code is long, and each form is in it four times.
 #pragma once
 
 #include <cstdint>
@@ -19,18 +26,27 @@ namespace bfa {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+constexpr int kTanhTerms = 7;
+constexpr float kTanhAnyMax = 9.f;
+
+// What a call makes of its scores.
+enum ScoreMode : int {
+  kScorePlain = 0,
+  kScoreCap = 1,
+  kScoreSlopes = 2,
+  kScoreCapSlopes = 3,
+};
+
 // Device view of a call's score shape (all zero: plain scores).
 struct ScoreParams {
   float c0;             // scale / cap
   float c1;             // cap * log2(e)  (0: no cap)
+  float ninv_c1_sq;     // -1 / c1^2
+  float poly_max;       // largest |s| for the polynomial (negative: not to be used)
+  float poly[kTanhTerms];  // its coefficients in s^2, times c1 c0
   const float* slopes;  // [H] or nullptr
+  __host__ __device__ int mode() const { return (c1 != 0.f ? kScoreCap : 0) | (slopes ? kScoreSlopes : 0); }
 };
-
-constexpr float kTanhPoly = 0.75f;
-constexpr int kTanhTerms = 6;
-// coefficients of P in u = x^2, lowest first
-__device__ constexpr float kTanhC[kTanhTerms] = {0.999999971f,   -0.333329589f, 0.13325406f,
-                                                 -0.0533444299f, 0.0195829077f, -0.00471625689f};
 
 __device__ __forceinline__ float rcp_approx(float x) {
   float y;
@@ -38,29 +54,54 @@ __device__ __forceinline__ float rcp_approx(float x) {
   return y;
 }
 
-// tanh of |x| <= kTanhPoly
-__device__ __forceinline__ float tanh_small(float x) {
-  const float u = x * x;
-  float p = kTanhC[kTanhTerms - 1];
+// cap * tanh(c0 s) * log2(e) of a pair: the folded polynomial
+__device__ __forceinline__ uint64_t capped_poly(uint64_t s, const ScoreParams& sp) {
+  const uint64_t u = ptx::f2_mul(s, s);
+  uint64_t p = ptx::f2_pack(sp.poly[kTanhTerms - 1], sp.poly[kTanhTerms - 1]);
 #pragma unroll
-  for (int i = kTanhTerms - 2; i >= 0; --i) p = fmaf(p, u, kTanhC[i]);
-  return x * p;
+  for (int i = kTanhTerms - 2; i >= 0; --i) p = ptx::f2_fma(p, u, ptx::f2_pack(sp.poly[i], sp.poly[i]));
+  return ptx::f2_mul(s, p);
 }
 
-// tanh of any x (infinities give +-1, NaN stays NaN)
-__device__ __forceinline__ float tanh_any(float x) {
-  const float a = fabsf(x);
-  const float big = 1.f - 2.f * rcp_approx(1.f + ptx::ex2_approx(2.f * kLog2e * a));
-  return a <= kTanhPoly ? tanh_small(x) : copysignf(big, x);
+// A constant pair made where it is used: the compiler would otherwise hold the pairs of
+// the rarer forms in registers over the whole tile loop, which costs the common one.
+__device__ __forceinline__ uint64_t f2_both(float c) {
+  uint64_t r;
+  asm volatile("mov.b64 %0, {%1, %1};" : "=l"(r) : "f"(c));
+  return r;
 }
 
-// two tanh values at once, |x| <= kTanhPoly (packed fp32 pairs)
-__device__ __forceinline__ uint64_t tanh_small2(uint64_t x) {
-  const uint64_t u = ptx::f2_mul(x, x);
-  uint64_t p = ptx::f2_pack(kTanhC[kTanhTerms - 1], kTanhC[kTanhTerms - 1]);
-#pragma unroll
-  for (int i = kTanhTerms - 2; i >= 0; --i) p = ptx::f2_fma(p, u, ptx::f2_pack(kTanhC[i], kTanhC[i]));
-  return ptx::f2_mul(x, p);
+// any x (infinities give the cap; NaN comes out as a cap, which only masked scores may be)
+__device__ __forceinline__ uint64_t capped_any2(float s0, float s1, const ScoreParams& sp) {
+  const float x0 = fminf(fmaxf(s0 * sp.c0, -kTanhAnyMax), kTanhAnyMax);
+  const float x1 = fminf(fmaxf(s1 * sp.c0, -kTanhAnyMax), kTanhAnyMax);
+  const uint64_t x = ptx::f2_pack(x0, x1), u = ptx::f2_mul(x, x);
+  uint64_t p = f2_both(1.3353410699e-08f), q = f2_both(7.7760461556e-07f);
+  p = ptx::f2_fma(p, u, f2_both(2.0608182991e-05f));
+  q = ptx::f2_fma(q, u, f2_both(3.2855461444e-04f));
+  p = ptx::f2_fma(p, u, f2_both(3.4955344269e-03f));
+  q = ptx::f2_fma(q, u, f2_both(2.5876779672e-02f));
+  p = ptx::f2_fma(p, u, f2_both(0.13380981060f));
+  q = ptx::f2_fma(q, u, f2_both(0.46714296718f));
+  p = ptx::f2_fma(p, u, f2_both(0.99999997963f));
+  q = ptx::f2_fma(q, u, f2_both(1.f));
+  float q0, q1;
+  ptx::f2_unpack(q, q0, q1);
+  return ptx::f2_mul(ptx::f2_mul(ptx::f2_mul(x, f2_both(sp.c1)), p), ptx::f2_pack(rcp_approx(q0), rcp_approx(q1)));
+}
+
+__device__ __forceinline__ float capped_any(float s, const ScoreParams& sp) {
+  float a, b;
+  ptx::f2_unpack(capped_any2(s, s, sp), a, b);
+  return a;
+}
+
+enum CapForm : int { kCapPoly = 0, kCapAny = 1 };
+
+template <int kForm>
+__device__ __forceinline__ uint64_t capped_pair(float s0, float s1, const ScoreParams& sp) {
+  if (kForm == kCapPoly) return capped_poly(ptx::f2_pack(s0, s1), sp);
+  return capped_any2(s0, s1, sp);
 }
 
 // The penalty along one row (or column) of a tile: -slope * |d0 + step * j| for
@@ -91,110 +132,115 @@ __device__ __forceinline__ float bias_at(const ScoreBias& r, int j) {
   return -r.slope * fabsf(fmaf(r.step, static_cast<float>(j), r.d0));
 }
 
-// A row of 128 products s becomes shaped scores in log2 units, in place (the
-// forward: one row a thread).  Called by whole warps.
-__device__ __forceinline__ void shape_row(float* s, const ScoreParams& sp, float scale_log2, float slope, int d0) {
-  if (sp.c1 != 0.f) {
-    float mx[4] = {0.f, 0.f, 0.f, 0.f};
+// a pair of products with the cap (or the scale) and a linear penalty: log2 units
+template <int kMode, int kForm>
+__device__ __forceinline__ uint64_t shaped_linear(float s0, float s1, int j, const ScoreBias& r, const ScoreParams& sp,
+                                                  float scale_log2) {
+  if (kMode == kScoreCap) return capped_pair<kForm>(s0, s1, sp);
+  const uint64_t bias = ptx::f2_pack(fmaf(r.b, static_cast<float>(j), r.a), fmaf(r.b, static_cast<float>(j + 1), r.a));
+  if (kMode == kScoreSlopes) return ptx::f2_fma(ptx::f2_pack(s0, s1), ptx::f2_pack(scale_log2, scale_log2), bias);
+  return ptx::f2_add(capped_pair<kForm>(s0, s1, sp), bias);
+}
+
+template <int kMode, int kForm, bool kTurn>
+__device__ __forceinline__ void shape_row_as(float* s, const ScoreParams& sp, float scale_log2, const ScoreBias& r) {
 #pragma unroll
-    for (int j = 0; j < 128; j += 2)
-      mx[(j >> 1) & 3] = ptx::fmax3(mx[(j >> 1) & 3], fabsf(s[j]), fabsf(s[j + 1]));
-    const float big = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-    if (__all_sync(0xffffffffu, big * sp.c0 <= kTanhPoly)) {
-      const uint64_t c0 = ptx::f2_pack(sp.c0, sp.c0), c1 = ptx::f2_pack(sp.c1, sp.c1);
-#pragma unroll
-      for (int j = 0; j < 128; j += 2)
-        ptx::f2_unpack(ptx::f2_mul(tanh_small2(ptx::f2_mul(ptx::f2_pack(s[j], s[j + 1]), c0)), c1), s[j], s[j + 1]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 128; ++j) s[j] = sp.c1 * tanh_any(s[j] * sp.c0);
-    }
-  }
-  if (sp.slopes) {
-    const float mul = sp.c1 != 0.f ? 1.f : scale_log2;
-    const ScoreBias r = score_bias(slope, d0, -1);
-    if (r.linear) {
-      const uint64_t mul2 = ptx::f2_pack(mul, mul);
-#pragma unroll
-      for (int j = 0; j < 128; j += 2)
-        ptx::f2_unpack(ptx::f2_fma(ptx::f2_pack(s[j], s[j + 1]), mul2,
-                                   ptx::f2_pack(fmaf(r.b, static_cast<float>(j), r.a),
-                                                fmaf(r.b, static_cast<float>(j + 1), r.a))),
-                       s[j], s[j + 1]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 128; ++j) s[j] = fmaf(s[j], mul, bias_at(r, j));
+  for (int j = 0; j < 128; j += 2) {
+    if (!kTurn) {
+      ptx::f2_unpack(shaped_linear<kMode, kForm>(s[j], s[j + 1], j, r, sp, scale_log2), s[j], s[j + 1]);
+    } else {  // the penalty changes direction in this tile
+      float z0 = s[j] * scale_log2, z1 = s[j + 1] * scale_log2;
+      if (kMode & kScoreCap) ptx::f2_unpack(capped_pair<kForm>(s[j], s[j + 1], sp), z0, z1);
+      s[j] = z0 + bias_at(r, j);
+      s[j + 1] = z1 + bias_at(r, j + 1);
     }
   }
 }
 
-// How the backward treats a group of scores: no cap; a cap with every |x| within
-// the polynomial's range; a cap with any x.
-enum ScoreTanh { kTanhNone = 0, kTanhSmall = 1, kTanhAny = 2 };
+// A row of 128 products s becomes shaped scores in log2 units, in place (the
+// forward: one row a thread).  Called by whole warps.
+template <int kMode>
+__device__ __forceinline__ void shape_row(float* s, const ScoreParams& sp, float scale_log2, float slope, int d0) {
+  ScoreBias r = {};
+  r.linear = true;
+  if (kMode & kScoreSlopes) r = score_bias(slope, d0, -1);
+  if (!(kMode & kScoreCap)) {
+    if (r.linear) shape_row_as<kMode, kCapPoly, false>(s, sp, scale_log2, r);
+    else shape_row_as<kMode, kCapPoly, true>(s, sp, scale_log2, r);
+    return;
+  }
+  float mx[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 128; j += 2) mx[(j >> 1) & 3] = ptx::fmax3(mx[(j >> 1) & 3], fabsf(s[j]), fabsf(s[j + 1]));
+  const float big = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+  if (r.linear && __all_sync(0xffffffffu, big <= sp.poly_max)) shape_row_as<kMode, kCapPoly, false>(s, sp, scale_log2, r);
+  else shape_row_as<kMode, kCapAny, (kMode & kScoreSlopes) != 0>(s, sp, scale_log2, r);
+}
 
-// A pair of products (entries j, j + 1) as shaped scores z (log2 units), and the
-// cap's factor f = 1 - tanh^2 (untouched for kTanhNone).  kSlow also takes the
-// attend-bits of the group's 32 entries (bit jb for entry j: masked scores -inf,
-// their products not looked at) and penalties that change direction in the tile.
-template <int kTanh, bool kSlow>
+// The backward: a pair of products (entries j, j + 1) as the exponents x of their
+// weights, log2(P) = z - LSE (nl: minus LSE log2 e of the two), and the cap's factor
+// f = 1 - tanh^2 (untouched without a cap).  kSlow also takes the attend-bits of
+// the group's 32 entries (bit jb for entry j: masked ones -inf, their products not
+// looked at) and penalties that change direction in the tile.
+template <int kMode, int kForm, bool kSlow>
 __device__ __forceinline__ void shape_pair(float s0, float s1, int j, int jb, uint32_t bits, const ScoreBias& r,
-                                           const ScoreParams& sp, float scale_log2, uint64_t& z, uint64_t& f) {
+                                           const ScoreParams& sp, float scale_log2, uint64_t nl, uint64_t& x,
+                                           uint64_t& f) {
   if (kSlow) {
     if (!((bits >> jb) & 1u)) s0 = 0.f;
     if (!((bits >> (jb + 1)) & 1u)) s1 = 0.f;
   }
-  const uint64_t bias = kSlow ? ptx::f2_pack(bias_at(r, j), bias_at(r, j + 1))
-                              : ptx::f2_pack(fmaf(r.b, static_cast<float>(j), r.a),
-                                             fmaf(r.b, static_cast<float>(j + 1), r.a));
-  if (kTanh == kTanhNone) {
-    z = ptx::f2_fma(ptx::f2_pack(s0, s1), ptx::f2_pack(scale_log2, scale_log2), bias);
+  if (kMode & kScoreSlopes) {
+    const uint64_t bias = kSlow ? ptx::f2_pack(bias_at(r, j), bias_at(r, j + 1))
+                                : ptx::f2_pack(fmaf(r.b, static_cast<float>(j), r.a),
+                                               fmaf(r.b, static_cast<float>(j + 1), r.a));
+    nl = ptx::f2_add(nl, bias);
+  }
+  if (kMode & kScoreCap) {
+    const uint64_t z = capped_pair<kForm>(s0, s1, sp);
+    x = ptx::f2_add(z, nl);
+    f = ptx::f2_fma(ptx::f2_mul(z, ptx::f2_pack(sp.ninv_c1_sq, sp.ninv_c1_sq)), z, ptx::f2_pack(1.f, 1.f));
   } else {
-    const uint64_t x = ptx::f2_mul(ptx::f2_pack(s0, s1), ptx::f2_pack(sp.c0, sp.c0));
-    uint64_t t;
-    if (kTanh == kTanhSmall) {
-      t = tanh_small2(x);
-    } else {
-      float x0, x1;
-      ptx::f2_unpack(x, x0, x1);
-      t = ptx::f2_pack(tanh_any(x0), tanh_any(x1));
-    }
-    z = ptx::f2_fma(t, ptx::f2_pack(sp.c1, sp.c1), bias);
-    f = ptx::f2_fma(ptx::f2_mul(t, ptx::f2_pack(-1.f, -1.f)), t, ptx::f2_pack(1.f, 1.f));
+    x = ptx::f2_fma(ptx::f2_pack(s0, s1), ptx::f2_pack(scale_log2, scale_log2), nl);
   }
   if (kSlow) {
-    float z0, z1;
-    ptx::f2_unpack(z, z0, z1);
-    if (!((bits >> jb) & 1u)) z0 = -INFINITY;
-    if (!((bits >> (jb + 1)) & 1u)) z1 = -INFINITY;
-    z = ptx::f2_pack(z0, z1);
+    float x0, x1;
+    ptx::f2_unpack(x, x0, x1);
+    if (!((bits >> jb) & 1u)) x0 = -INFINITY;
+    if (!((bits >> (jb + 1)) & 1u)) x1 = -INFINITY;
+    x = ptx::f2_pack(x0, x1);
   }
 }
 
-// Which form a group of 32 products takes (warp-uniform); masked ones count too:
-// they only cost the choice.
-__device__ __forceinline__ int score_form(const uint32_t (&s)[32], const ScoreParams& sp) {
-  if (sp.c1 == 0.f) return kTanhNone;
-  float mx = 0.f;
-#pragma unroll
-  for (int j = 0; j < 32; j += 2) mx = ptx::fmax3(mx, fabsf(__uint_as_float(s[j])), fabsf(__uint_as_float(s[j + 1])));
-  return __all_sync(0xffffffffu, mx * sp.c0 <= kTanhPoly) ? kTanhSmall : kTanhAny;
-}
-
-// Run body(form tag, slow tag) for the form at hand.
+// Run body(form tag, slow tag) for a group of 32 products: the cap's form by their largest
+// magnitude (masked ones count too: they only cost the choice).  Called by whole warps.
 template <int V>
 struct ScoreTag {
   static constexpr int value = V;
 };
-template <typename F>
-__device__ __forceinline__ void score_dispatch(int form, bool slow, F&& body) {
-  if (form == kTanhNone) {
-    if (slow) body(ScoreTag<kTanhNone>(), ScoreTag<1>());
-    else body(ScoreTag<kTanhNone>(), ScoreTag<0>());
-  } else if (form == kTanhSmall) {
-    if (slow) body(ScoreTag<kTanhSmall>(), ScoreTag<1>());
-    else body(ScoreTag<kTanhSmall>(), ScoreTag<0>());
+template <int kMode, typename F>
+__device__ __forceinline__ void score_dispatch(const uint32_t (&s)[32], const ScoreParams& sp, bool slow, F&& body) {
+  if (kMode & kScoreCap) {
+    float mx = 0.f;
+#pragma unroll
+    for (int j = 0; j < 32; j += 2)
+      mx = ptx::fmax3(mx, fabsf(__uint_as_float(s[j])), fabsf(__uint_as_float(s[j + 1])));
+    if (slow || !__all_sync(0xffffffffu, mx <= sp.poly_max)) body(ScoreTag<kCapAny>(), ScoreTag<1>());
+    else body(ScoreTag<kCapPoly>(), ScoreTag<0>());
   } else {
-    body(ScoreTag<kTanhAny>(), ScoreTag<1>());
+    if (slow) body(ScoreTag<kCapPoly>(), ScoreTag<1>());
+    else body(ScoreTag<kCapPoly>(), ScoreTag<0>());
+  }
+}
+
+// f(mode tag) for a call's mode (host)
+template <typename F>
+inline auto for_score_mode(int mode, F&& f) {
+  switch (mode) {
+    case kScoreCap: return f(ScoreTag<kScoreCap>());
+    case kScoreSlopes: return f(ScoreTag<kScoreSlopes>());
+    case kScoreCapSlopes: return f(ScoreTag<kScoreCapSlopes>());
+    default: return f(ScoreTag<kScorePlain>());
   }
 }
 
