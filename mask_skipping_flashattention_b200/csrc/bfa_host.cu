@@ -1003,25 +1003,31 @@ int sm_count() {
 ScoreParams score_params(float scale, float softcap, const float* slopes) {
   static const double kTerms[kTanhTerms] = {0.99999995,   -0.333328392,   0.133252041,  -0.0534570294,
                                             0.0202899801, -0.00620337882, 0.00104102254};
+  static const double kFew[kTanhFew] = {0.999999893, -0.333319542, 0.13304526, -0.0518218664, 0.0150509448};
   ScoreParams sp;
   std::memset(&sp, 0, sizeof(sp));
   sp.slopes = slopes;
-  sp.poly_max = -1.f;
+  sp.poly_max = sp.few_max = -1.f;
   if (!(softcap > 0.f)) return sp;
   const double c0 = static_cast<double>(scale) / softcap, c1 = static_cast<double>(softcap) * 1.4426950408889634;
   sp.c0 = static_cast<float>(c0);
   sp.c1 = static_cast<float>(c1);
   sp.ninv_c1_sq = static_cast<float>(-1.0 / (c1 * c1));
-  // The folded polynomial serves |x| <= 1; where a small c0 (a large cap) pushes its last
-  // coefficients below what fp32 holds well, only as far as their terms do not count.
-  double x_max = 1.0, most = 0.0;
-  for (int k = 0; k < kTanhTerms; ++k) {
-    const double v = kTerms[k] * c1 * std::pow(c0, 2 * k + 1);
-    sp.poly[k] = static_cast<float>(v);
-    most = std::max(most, std::fabs(v));
-    if (std::fabs(v) < 1e-38) x_max = std::min(x_max, k == 0 ? 0.0 : std::pow(1e-8 / std::fabs(kTerms[k]), 0.5 / k));
-  }
-  if (x_max > 0 && sp.c0 > 0.f && most < 1e30) sp.poly_max = static_cast<float>(std::min(x_max / c0, 1e15));
+  // The folded polynomials serve |x| <= 1 and 0.625; where a small c0 (a large cap) pushes
+  // the last coefficients below what fp32 holds well, only as far as their terms do not count.
+  auto fold = [&](const double* terms, int n, double x_max, float* out) -> float {
+    double most = 0.0;
+    for (int k = 0; k < n; ++k) {
+      const double v = terms[k] * c1 * std::pow(c0, 2 * k + 1);
+      out[k] = static_cast<float>(v);
+      most = std::max(most, std::fabs(v));
+      if (std::fabs(v) < 1e-38) x_max = std::min(x_max, k == 0 ? 0.0 : std::pow(1e-8 / std::fabs(terms[k]), 0.5 / k));
+    }
+    if (!(x_max > 0 && sp.c0 > 0.f && most < 1e30)) return -1.f;
+    return static_cast<float>(std::min(x_max / c0, 1e15));
+  };
+  sp.poly_max = fold(kTerms, kTanhTerms, 1.0, sp.poly);
+  sp.few_max = fold(kFew, kTanhFew, 0.625, sp.few);
   return sp;
 }
 

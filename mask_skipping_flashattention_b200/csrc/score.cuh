@@ -4,18 +4,21 @@
 // cap's chain rule puts on the score gradient.
 //
 // tanh(x), x = c0 s with c0 = scale / cap, from minimax fits of tanh(x) / x in u = x^2:
-//   |x| <= 1  7 terms, relative error 5e-8 (1.6e-7 as evaluated in fp32);
-//   any x     5 terms over 5, to |x| = 9 (then constant), 2e-8 (3.3e-7).
+//   |x| <= 0.625  5 terms, relative error 1.1e-7 (2.1e-7 as evaluated in fp32);
+//   |x| <= 1      7 terms, 5e-8 (1.6e-7);
+//   any x         5 terms over 5, to |x| = 9 (then constant), 2e-8 (3.3e-7).
 // They keep the score's error proportional to the score, which the hardware's tanh
 // (relative 2^-11) would not: with a cap of 50 that one moves a score by up to 0.02 and
-// its weight by 2 %.  In the first, scale, cap and log2 e are folded into the
-// coefficients, so that a score costs its square, the terms and one product: the
-// softmax warps are bound by the instructions they issue (about 3 a score without a
-// shape; 7 and 12 with these).  Which form a group of scores takes is decided by its
-// largest magnitude, a warp at a time.  More forms were slower: with 5 folded terms to
-// 0.625 and 8 to 1 beside the last, a backward that stays in the 8-term form takes 1628 us
-// (4 x 4096 tokens, 16 / 4 heads, D 128), with the 8-term and the last form alone 1264 us: the
-// kernel's code is long, and each form is in it four times.
+// its weight by 2 %.  In the polynomials, scale, cap and log2 e are folded into the
+// coefficients, so that a score costs its square, the terms and one product; the fp32 pipe
+// is what they load (two operations a score without a shape; 8, 10 and some 14 and a
+// reciprocal with these), beside the exponential of the special-function unit.
+// Which form a group of scores takes is decided by its largest magnitude, a warp at a
+// time.  Measured, causal 8192 row, 16 / 4 heads, D 128: forward 292 us without a shape, 406,
+// 472 and 706 us in the three forms; backward 1110 us in the 7 terms, 1563 in the last.  The
+// backward leaves the 5 terms out: each form is four times in its code, and groups
+// that alternate between three forms made it slower (1121 -> 1322 us at a cap that splits
+// them) than the two terms saved.
 #pragma once
 
 #include <cstdint>
@@ -26,7 +29,7 @@ namespace bfa {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-constexpr int kTanhTerms = 7;
+constexpr int kTanhTerms = 7, kTanhFew = 5;
 constexpr float kTanhAnyMax = 9.f;
 
 // What a call makes of its scores.
@@ -44,6 +47,8 @@ struct ScoreParams {
   float ninv_c1_sq;     // -1 / c1^2
   float poly_max;       // largest |s| for the polynomial (negative: not to be used)
   float poly[kTanhTerms];  // its coefficients in s^2, times c1 c0
+  float few_max;        // the same for the shorter one
+  float few[kTanhFew];
   const float* slopes;  // [H] or nullptr
   __host__ __device__ int mode() const { return (c1 != 0.f ? kScoreCap : 0) | (slopes ? kScoreSlopes : 0); }
 };
@@ -55,11 +60,12 @@ __device__ __forceinline__ float rcp_approx(float x) {
 }
 
 // cap * tanh(c0 s) * log2(e) of a pair: the folded polynomial
-__device__ __forceinline__ uint64_t capped_poly(uint64_t s, const ScoreParams& sp) {
+template <int kTerms>
+__device__ __forceinline__ uint64_t capped_poly(uint64_t s, const float (&c)[kTerms]) {
   const uint64_t u = ptx::f2_mul(s, s);
-  uint64_t p = ptx::f2_pack(sp.poly[kTanhTerms - 1], sp.poly[kTanhTerms - 1]);
+  uint64_t p = ptx::f2_pack(c[kTerms - 1], c[kTerms - 1]);
 #pragma unroll
-  for (int i = kTanhTerms - 2; i >= 0; --i) p = ptx::f2_fma(p, u, ptx::f2_pack(sp.poly[i], sp.poly[i]));
+  for (int i = kTerms - 2; i >= 0; --i) p = ptx::f2_fma(p, u, ptx::f2_pack(c[i], c[i]));
   return ptx::f2_mul(s, p);
 }
 
@@ -96,11 +102,12 @@ __device__ __forceinline__ float capped_any(float s, const ScoreParams& sp) {
   return a;
 }
 
-enum CapForm : int { kCapPoly = 0, kCapAny = 1 };
+enum CapForm : int { kCapPoly = 0, kCapAny = 1, kCapFew = 2 };
 
 template <int kForm>
 __device__ __forceinline__ uint64_t capped_pair(float s0, float s1, const ScoreParams& sp) {
-  if (kForm == kCapPoly) return capped_poly(ptx::f2_pack(s0, s1), sp);
+  if (kForm == kCapFew) return capped_poly(ptx::f2_pack(s0, s1), sp.few);
+  if (kForm == kCapPoly) return capped_poly(ptx::f2_pack(s0, s1), sp.poly);
   return capped_any2(s0, s1, sp);
 }
 
@@ -173,7 +180,8 @@ __device__ __forceinline__ void shape_row(float* s, const ScoreParams& sp, float
 #pragma unroll
   for (int j = 0; j < 128; j += 2) mx[(j >> 1) & 3] = ptx::fmax3(mx[(j >> 1) & 3], fabsf(s[j]), fabsf(s[j + 1]));
   const float big = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-  if (r.linear && __all_sync(0xffffffffu, big <= sp.poly_max)) shape_row_as<kMode, kCapPoly, false>(s, sp, scale_log2, r);
+  if (r.linear && __all_sync(0xffffffffu, big <= sp.few_max)) shape_row_as<kMode, kCapFew, false>(s, sp, scale_log2, r);
+  else if (r.linear && __all_sync(0xffffffffu, big <= sp.poly_max)) shape_row_as<kMode, kCapPoly, false>(s, sp, scale_log2, r);
   else shape_row_as<kMode, kCapAny, (kMode & kScoreSlopes) != 0>(s, sp, scale_log2, r);
 }
 
