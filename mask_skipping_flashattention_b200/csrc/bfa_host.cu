@@ -1334,6 +1334,16 @@ bfa_status bwd_launch_from_host(bfa_plan* P, const void* q, const void* k, const
     p.dq_acc = fused ? p.ws_d + ws_rows : nullptr;
   }
   BFA_CUDA(launch_bwd_prep(p, st), "backward preprocess kernel");
+  if (p.score.mode() != kScorePlain && P->max_nkt <= kRefineMaxTiles) {
+    // rows of few tiles there can be: the first query tiles of each group under a causal
+    // order, any under another mask
+    int64_t rows = P->n_rows;
+    if (P->kind == BFA_PLAN_POSITIONAL && P->window < 0 && !P->groups_h.empty()) {
+      rows = 0;
+      for (const auto& g : P->groups_h) rows += g.nkt <= kRefineTiles ? g.nqt : std::min(g.nqt, kRefineTiles);
+    }
+    BFA_CUDA(launch_bwd_refine(D, tq, tdo, tk, tv, p, rows * p.rep, st), "backward refine kernel");
+  }
   if (fused) {
     BFA_CUDA(launch_bwd_fused(tk, tv, tq, tdo, p, static_cast<int64_t>(n_cols) * p.rep_kv, st), "fused backward kernel");
     BFA_CUDA(launch_bwd_dq_store(p, st), "dQ store kernel");

@@ -276,7 +276,15 @@ struct DqWork {
 // the previous tile's dQ products may still read.
 constexpr int kDqThreads = 384;
 
-template <int D, int kScore>
+// kRefine (shaped scores): the same walk, but instead of dQ it sums, per row,
+// r = sum_j P (dP - D), which is what D = dO . O misses because O went through bf16
+// twice (as P before P V, and as the output): sum_j P dP is D + r.  A row that
+// attends few keys has dP - D near 0 wherever its weight is near 1, so there the error is the
+// gradient's: documents of some 20 tokens with a cap had dQ and dK off by 0.0056 (2-norm),
+// 0.0037 refined; rounding alone gives 0.002.  Rows of up to kRefineTiles key tiles are
+// refined, in calls whose longest row has kRefineMaxTiles (longer rows average the error
+// out, 0.004 at 64 tiles, and refining the few short ones among them changes nothing).
+template <int D, int kScore, bool kRefine>
 __global__ void __launch_bounds__(kDqThreads, 1)
     k_bwd_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
              const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const BwdParams p) {
@@ -298,6 +306,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ DqWork wk_s;
+  __shared__ float half_s[kRefine ? kTile : 1];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
   auto sK = [&](int st) { return sK0 + st * C::kTileBytes; };
@@ -308,7 +317,12 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     for (int i = 0; i < NBAR; ++i) mbar_init(bar(i), (i == BC || i == BP || i == BP + 1) ? 8 : 1);
     fence_barrier_init();
     int i, j;
-    chunked_decode(blockIdx.x, p.plan.n_rows, p.rep, p.head_chunk, i, j);
+    if constexpr (kRefine) {  // the shortest rows: the end of the order
+      i = p.plan.n_rows - 1 - static_cast<int>(blockIdx.x / static_cast<unsigned>(p.rep));
+      j = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.rep));
+    } else {
+      chunked_decode(blockIdx.x, p.plan.n_rows, p.rep, p.head_chunk, i, j);
+    }
     uint32_t* const err = p.plan.err;
     (void)err;
     const int2 rw = p.plan.row_work[BFA_IDX(i, p.plan.n_rows, err)];  // {row, its group}, longest first
@@ -332,6 +346,10 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     replica_bh(p, w.g, j, w.b, w.h);
     w.hk = w.h / (p.H / p.Hkv);
     wk_s = w;
+  }
+  if constexpr (kRefine) {
+    __syncthreads();
+    if (wk_s.n == 0 || wk_s.n > kRefineTiles) return;
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(&tmem_slot), C::kTmemCols);
@@ -398,6 +416,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         issue_nn<D>(tdP, sdO, sV(0));  // dP = dO V^T
         umma_commit(bar(BS));
         umma_commit(bar(VE + 0));
+        if (kRefine) umma_commit(bar(KE + 0));
       }
       for (int u = 0; ok && u < n; ++u) {
         const int sk = u % kDqKStages;
@@ -411,7 +430,9 @@ __global__ void __launch_bounds__(kDqThreads, 1)
           issue_nn<D>(tdP, sdO, sV(st1));
           umma_commit(bar(BS));
           umma_commit(bar(VE + st1));
+          if (kRefine) umma_commit(bar(KE + (u + 1) % kDqKStages));
         }
+        if (kRefine) continue;  // no dS, no dQ
         if (!mbar_wait_fast(bar(BP + (u & 1)), (u >> 1) & 1, cap, &abort_flag)) { ok = false; break; }
         tc_fence_after();
         const uint64_t dk = mn_desc(sK(sk));
@@ -439,6 +460,7 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     if constexpr ((kScore & kScoreSlopes) != 0) slope = __ldg(p.score.slopes + wk.h) * kLog2e;
     (void)slope;
     bool ok = true;
+    float r = 0.f;  // kRefine
     int kt_next = n > 0 ? p.plan.kv_tile[wk.e0] : 0;
     int part_next = n > 0 ? p.plan.part[wk.e0] : -1;
     for (int u = 0; u < n; ++u) {
@@ -489,14 +511,15 @@ __global__ void __launch_bounds__(kDqThreads, 1)
               float x0, x1, d0, d1;
               f2_unpack(x, x0, x1);
               w = f2_pack(ex2_approx(x0), ex2_approx(x1));
-              if (kScore & kScoreCap) w = f2_mul(w, f);
+              if ((kScore & kScoreCap) && !kRefine) w = f2_mul(w, f);
               f2_unpack(f2_mul(w, f2_add(f2_pack(__uint_as_float(dv[cc][c0]), __uint_as_float(dv[cc][c0 + 1])),
                                          f2_pack(nd, nd))),
                         d0, d1);
-              pk[jj] = pack_bf16x2(d0, d1);
+              if (kRefine) r += d0 + d1;
+              else pk[jj] = pack_bf16x2(d0, d1);
             }
           });
-          tmem_st_32x32b_x16(tdS + gc * 16, pk);
+          if constexpr (!kRefine) tmem_st_32x32b_x16(tdS + gc * 16, pk);
           continue;
         }
         if (masked) {  // masked scores become -inf, so 2^(...) is 0 (partial and edge tiles only)
@@ -515,13 +538,20 @@ __global__ void __launch_bounds__(kDqThreads, 1)
         }
         tmem_st_32x32b_x16(tdS + gc * 16, pk);
       }
+      if (kRefine) continue;
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(BP + (u & 1)));
     }
-    bool done = ok;
-    if (ok && n > 0) {
+    if constexpr (kRefine) {
+      if (half == 1) half_s[row] = r;
+      named_bar_sync(1, 256);
+      // D of this row (stored negated); rows past the sequence stay 0
+      if (half == 0 && ok && qpos < wk.g.q_len) p.ws_d[wi] = nd - (r + half_s[row]);
+    }
+    bool done = ok && !kRefine;
+    if (done && n > 0) {
       const bool got = mbar_wait(bar(BO), 0, cap, &abort_flag);
       done = !__any_sync(0xffffffffu, !got);
     }
@@ -1365,13 +1395,13 @@ static cudaError_t bwd_prepare(K kernel, int smem) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 
-template <int D, int kScore>
+template <int D, int kScore, bool kRefine>
 static cudaError_t launch_dq_as(const CUtensorMap& tq, const CUtensorMap& tdo, const CUtensorMap& tk,
                                 const CUtensorMap& tv, const BwdParams& p, int64_t n_work, cudaStream_t s) {
   static DeviceOnce once;
-  const cudaError_t e = once.run([] { return bwd_prepare(k_bwd_dq<D, kScore>, BCfg<D>::kDqSmemBytes); });
+  const cudaError_t e = once.run([] { return bwd_prepare(k_bwd_dq<D, kScore, kRefine>, BCfg<D>::kDqSmemBytes); });
   if (e != cudaSuccess) return e;
-  k_bwd_dq<D, kScore><<<static_cast<unsigned>(n_work), kDqThreads, BCfg<D>::kDqSmemBytes, s>>>(tq, tdo, tk, tv, p);
+  k_bwd_dq<D, kScore, kRefine><<<static_cast<unsigned>(n_work), kDqThreads, BCfg<D>::kDqSmemBytes, s>>>(tq, tdo, tk, tv, p);
   return cudaGetLastError();
 }
 
@@ -1379,7 +1409,7 @@ template <int D>
 static cudaError_t launch_dq_one(const CUtensorMap& tq, const CUtensorMap& tdo, const CUtensorMap& tk,
                                  const CUtensorMap& tv, const BwdParams& p, int64_t n_work, cudaStream_t s) {
   return for_score_mode(p.score.mode(), [&](auto mode) {
-    return launch_dq_as<D, decltype(mode)::value>(tq, tdo, tk, tv, p, n_work, s);
+    return launch_dq_as<D, decltype(mode)::value, false>(tq, tdo, tk, tv, p, n_work, s);
   });
 }
 
@@ -1399,6 +1429,25 @@ static cudaError_t launch_dkdv_one(const CUtensorMap& tk, const CUtensorMap& tv,
   return for_score_mode(p.score.mode(), [&](auto mode) {
     return launch_dkdv_as<D, decltype(mode)::value>(tk, tv, tq, tdo, p, n_work, s);
   });
+}
+
+template <int D>
+static cudaError_t launch_refine_one(const CUtensorMap& tq, const CUtensorMap& tdo, const CUtensorMap& tk,
+                                     const CUtensorMap& tv, const BwdParams& p, int64_t n_work, cudaStream_t s) {
+  switch (p.score.mode()) {
+    case kScoreCap: return launch_dq_as<D, kScoreCap, true>(tq, tdo, tk, tv, p, n_work, s);
+    case kScoreSlopes: return launch_dq_as<D, kScoreSlopes, true>(tq, tdo, tk, tv, p, n_work, s);
+    case kScoreCapSlopes: return launch_dq_as<D, kScoreCapSlopes, true>(tq, tdo, tk, tv, p, n_work, s);
+    default: return cudaSuccess;  // plain scores keep the D of the preprocess
+  }
+}
+
+cudaError_t launch_bwd_refine(int D, const CUtensorMap& tq, const CUtensorMap& tdo, const CUtensorMap& tk,
+                              const CUtensorMap& tv, const BwdParams& p, int64_t n_work, cudaStream_t s) {
+  if (n_work <= 0) return cudaSuccess;
+  if (n_work > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  return D == 64 ? launch_refine_one<64>(tq, tdo, tk, tv, p, n_work, s)
+                 : launch_refine_one<128>(tq, tdo, tk, tv, p, n_work, s);
 }
 
 cudaError_t launch_bwd_dq(int D, const CUtensorMap& tq, const CUtensorMap& tdo, const CUtensorMap& tk,

@@ -59,6 +59,11 @@ struct BwdParams {
 };
 
 cudaError_t launch_bwd_prep(const BwdParams& p, cudaStream_t s);
+// shaped scores: D of the rows of few key tiles, from the scores (after the preprocess), for
+// the last n_work / rep rows of the plan's order
+constexpr int kRefineTiles = 2, kRefineMaxTiles = 16;
+cudaError_t launch_bwd_refine(int D, const CUtensorMap& tq, const CUtensorMap& tdo, const CUtensorMap& tk,
+                              const CUtensorMap& tv, const BwdParams& p, int64_t n_work, cudaStream_t s);
 cudaError_t launch_bwd_dq(int D, const CUtensorMap& tq, const CUtensorMap& tdo, const CUtensorMap& tk,
                           const CUtensorMap& tv, const BwdParams& p, int64_t n_work, cudaStream_t s);
 cudaError_t launch_bwd_dkdv(int D, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,

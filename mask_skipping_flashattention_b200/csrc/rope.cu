@@ -7,9 +7,11 @@
 // 1e-11 turns at position 10^6, where a product in fp32 would be off by 0.06
 // radians.
 //
-// Bound by HBM: two bytes in and two out a value.  A thread owns one 16-byte
-// chunk pair of a token (8 pairs: one cos / sin evaluation each) and walks the
-// heads with it, so the trigonometry is paid once for `heads_per_thread` heads.
+// Bound by HBM: two bytes in and two out a value.  A thread owns one chunk pair of a
+// head (two 16-byte chunks, 8 pairs) or one chunk that is copied, of one token, in every
+// kHeadLanes-th head: the trigonometry is paid once for all of them, neighbouring
+// threads cover kHeadLanes whole heads (1 KB at D 128), and kBatch heads are loaded before
+// the first is stored.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -22,6 +24,10 @@ namespace bfa {
 using namespace ptx;
 
 namespace {
+
+constexpr int kRopeThreads = 256;
+constexpr int kHeadLanes = 4;
+constexpr int kBatch = 4;
 
 __device__ __forceinline__ float2 bf2_to_f2(uint32_t u) {
   return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
@@ -40,19 +46,23 @@ __device__ __forceinline__ int seq_of_token(const int32_t* cu, int n_seq, int64_
 
 }  // namespace
 
-__global__ void __launch_bounds__(256) k_rope(const RopeParams p) {
-  const int pairs = p.rotary / 16;               // chunk pairs of a head that turn
-  const int chunks = pairs + (p.D - p.rotary) / 8;  // and chunks that are copied
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x;
-  const int64_t tok = id / chunks;
-  const int c = static_cast<int>(id - tok * chunks);
+// kRagged: positions and places from a ragged batch's lengths, keys and values into a cache
+template <bool kRagged>
+__global__ void __launch_bounds__(kRopeThreads) k_rope(const RopeParams p) {
+  const unsigned pairs = p.rotary / 16;                    // chunk pairs of a head that turn
+  const unsigned chunks = pairs + (p.D - p.rotary) / 8;    // and chunks that are copied
+  const unsigned lanes = chunks * kHeadLanes;              // threads of a token
+  const int64_t id = static_cast<int64_t>(blockIdx.x) * kRopeThreads + threadIdx.x;
+  const int64_t tok = id / lanes;
+  const unsigned in_tok = static_cast<unsigned>(id - tok * lanes);
+  const unsigned c = in_tok % chunks;
   if (tok >= p.tokens) return;
-  const int64_t b = tok / p.S, st = tok - b * p.S;
+  const int64_t b = kRagged ? 0 : tok / p.S, st = tok - b * p.S;
 
   // position of the token, and its place in the cache
   int64_t pos;
   int64_t row = -1;  // element offset of the token's cache row, or -1
-  if (p.positions) {
+  if constexpr (!kRagged) {
     const int64_t i = b * p.pos_sb + st;
     pos = p.positions64 ? static_cast<const int64_t*>(p.positions)[i]
                         : static_cast<int64_t>(static_cast<const int32_t*>(p.positions)[i]);
@@ -62,10 +72,10 @@ __global__ void __launch_bounds__(256) k_rope(const RopeParams p) {
     const int first = __ldg(p.cu_seqlens + s), end = __ldg(p.cu_seqlens + s + 1);
     if (tok < first) return;
     pos = static_cast<int64_t>(__ldg(p.seqused_k + s)) - (end - first) + (tok - first);
-    const int64_t pi = pos / p.page_size;
-    if (pos >= 0 && pi < p.pages_per_seq) {
+    if (pos >= 0 && pos < static_cast<int64_t>(p.pages_per_seq) * p.page_size) {
+      const int pi = static_cast<int>(pos) / p.page_size;
       const int64_t page = __ldg(p.block_table + static_cast<int64_t>(s) * p.pages_per_seq + pi);
-      if (page >= 0 && page < p.num_pages) row = page * p.c_sp + (pos - pi * p.page_size) * p.c_st;
+      if (page >= 0 && page < p.num_pages) row = page * p.c_sp + (static_cast<int>(pos) - pi * p.page_size) * p.c_st;
     }
   }
 
@@ -80,7 +90,7 @@ __global__ void __launch_bounds__(256) k_rope(const RopeParams p) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       // turns, minus the nearest integer: in [-1/2, 1/2]
-      const double t = static_cast<double>(pos) * p.inv_freq[c * 8 + i] * 0.15915494309189533577;
+      const double t = static_cast<double>(pos) * __ldg(p.inv_freq + c * 8 + i) * 0.15915494309189533577;
       float sn, cs;
       sincospif(2.f * static_cast<float>(t - rint(t)), &sn, &cs);
       co[i] = cs * p.amplitude;
@@ -88,7 +98,7 @@ __global__ void __launch_bounds__(256) k_rope(const RopeParams p) {
     }
   }
 
-  auto rotate = [&](const uint4& A, const uint4& B, uint4& oa, uint4& ob) {
+  auto rotate = [&](uint4& A, uint4& B) {
     const uint32_t a[4] = {A.x, A.y, A.z, A.w}, bb[4] = {B.x, B.y, B.z, B.w};
     uint32_t ra[4], rb[4];
     if (p.interleaved) {
@@ -106,56 +116,68 @@ __global__ void __launch_bounds__(256) k_rope(const RopeParams p) {
         rb[i] = pack_bf16x2(x.x * si[2 * i] + y.x * co[2 * i], x.y * si[2 * i + 1] + y.y * co[2 * i + 1]);
       }
     }
-    oa = make_uint4(ra[0], ra[1], ra[2], ra[3]);
-    ob = make_uint4(rb[0], rb[1], rb[2], rb[3]);
+    A = make_uint4(ra[0], ra[1], ra[2], ra[3]);
+    B = make_uint4(rb[0], rb[1], rb[2], rb[3]);
   };
 
-  const int heads = p.H + 2 * p.Hkv;  // q, then k, then v
-  const int h0 = blockIdx.y * p.heads_per_thread, h1 = min(heads, h0 + p.heads_per_thread);
-#pragma unroll 4
-  for (int h = h0; h < h1; ++h) {
-    const __nv_bfloat16* src;
-    __nv_bfloat16* dst;
-    bool plain = !turn;
-    if (h < p.H) {
-      src = p.q + b * p.q_sb + st * p.q_ss + static_cast<int64_t>(h) * p.q_sh;
-      dst = p.q_out + b * p.qo_sb + st * p.qo_ss + static_cast<int64_t>(h) * p.qo_sh;
-    } else if (h < p.H + p.Hkv) {
-      src = p.k + tok * p.k_ss + static_cast<int64_t>(h - p.H) * p.k_sh;
-      dst = row < 0 ? nullptr : p.k_cache + row + static_cast<int64_t>(h - p.H) * p.c_sh;
-    } else {
-      src = p.v + tok * p.v_ss + static_cast<int64_t>(h - p.H - p.Hkv) * p.v_sh;
-      dst = row < 0 ? nullptr : p.v_cache + row + static_cast<int64_t>(h - p.H - p.Hkv) * p.c_sh;
-      plain = true;
-    }
-    if (dst == nullptr) continue;  // no page for this token
-    uint4 A = *reinterpret_cast<const uint4*>(src + ca), B = A;
-    if (turn) {
-      B = *reinterpret_cast<const uint4*>(src + cb);
-      if (!plain) {
-        const uint4 A0 = A, B0 = B;
-        rotate(A0, B0, A, B);
+  // heads of q, then k, then v
+  const int heads = kRagged ? p.H + 2 * p.Hkv : p.H;
+  const __nv_bfloat16* const q = p.q + b * p.q_sb + st * p.q_ss;
+  __nv_bfloat16* const qo = p.q_out + b * p.qo_sb + st * p.qo_ss;
+  const int h1 = min(heads, static_cast<int>(blockIdx.y + 1) * p.heads_per_block);
+  for (int h0 = blockIdx.y * p.heads_per_block + in_tok / chunks; h0 < h1; h0 += kHeadLanes * kBatch) {
+    uint4 A[kBatch], B[kBatch];
+    __nv_bfloat16* dst[kBatch];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int h = h0 + i * kHeadLanes;
+      const __nv_bfloat16* src;
+      dst[i] = nullptr;  // past the heads, or no place for this token
+      if (h >= h1) continue;
+      if (!kRagged || h < p.H) {
+        src = q + static_cast<int64_t>(h) * p.q_sh;
+        dst[i] = qo + static_cast<int64_t>(h) * p.qo_sh;
+      } else {
+        if (row < 0) continue;
+        const bool is_v = h >= p.H + p.Hkv;
+        const int64_t hk = h - p.H - (is_v ? p.Hkv : 0);
+        src = is_v ? p.v + tok * p.v_ss + hk * p.v_sh : p.k + tok * p.k_ss + hk * p.k_sh;
+        dst[i] = (is_v ? p.v_cache : p.k_cache) + row + hk * p.c_sh;
       }
-      *reinterpret_cast<uint4*>(dst + cb) = B;
+      A[i] = *reinterpret_cast<const uint4*>(src + ca);
+      if (turn) B[i] = *reinterpret_cast<const uint4*>(src + cb);
     }
-    *reinterpret_cast<uint4*>(dst + ca) = A;
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (!dst[i]) continue;
+      if (turn) {
+        if (!kRagged || h0 + i * kHeadLanes < p.H + p.Hkv) rotate(A[i], B[i]);  // values are copied
+        *reinterpret_cast<uint4*>(dst[i] + cb) = B[i];
+      }
+      *reinterpret_cast<uint4*>(dst[i] + ca) = A[i];
+    }
   }
 }
 
 cudaError_t launch_rope(const RopeParams& p0, int sms, cudaStream_t s) {
   RopeParams p = p0;
+  const bool ragged = p.positions == nullptr;
   const int heads = p.H + 2 * p.Hkv;
   if (p.tokens <= 0 || heads <= 0) return cudaSuccess;
-  const int64_t threads = p.tokens * (p.rotary / 16 + (p.D - p.rotary) / 8);
-  // heads a thread walks: all of them while that still gives every SM 2048 threads
+  const int64_t threads = p.tokens * kHeadLanes * (p.rotary / 16 + (p.D - p.rotary) / 8);
+  // a block's share of the heads: all of them while that still gives every SM 2048
+  // threads, at least one batch round otherwise
+  const int rounds = (heads + kHeadLanes - 1) / kHeadLanes;
   int64_t groups = (static_cast<int64_t>(sms) * 2048 + threads - 1) / threads;
-  groups = groups < 1 ? 1 : (groups > heads ? heads : groups);
-  p.heads_per_thread = static_cast<int>((heads + groups - 1) / groups);
-  const int64_t blocks = (threads + 255) / 256;
+  groups = groups < 1 ? 1 : (groups > rounds ? rounds : groups);
+  p.heads_per_block = static_cast<int>((rounds + groups - 1) / groups) * kHeadLanes;
+  const int64_t blocks = (threads + kRopeThreads - 1) / kRopeThreads;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  const unsigned gy = static_cast<unsigned>((heads + p.heads_per_thread - 1) / p.heads_per_thread);
+  const unsigned gy = static_cast<unsigned>((heads + p.heads_per_block - 1) / p.heads_per_block);
   if (gy > 65535u) return cudaErrorInvalidConfiguration;
-  k_rope<<<dim3(static_cast<unsigned>(blocks), gy), 256, 0, s>>>(p);
+  const dim3 grid(static_cast<unsigned>(blocks), gy);
+  if (ragged) k_rope<true><<<grid, kRopeThreads, 0, s>>>(p);
+  else k_rope<false><<<grid, kRopeThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 

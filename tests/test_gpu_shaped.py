@@ -257,3 +257,22 @@ def test_the_checked_build_finds_no_index_out_of_bounds():
                        cwd=ROOT, env=dict(os.environ, BFA_LIBRARY="checked"), capture_output=True, text=True,
                        timeout=900)
     assert r.returncode == 0, r.stdout[-3000:] + r.stderr[-1000:]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cap,with_slopes", SHAPES)
+def test_a_row_with_a_single_key_has_no_query_gradient(D, cap, with_slopes):
+    # its weight is 1 whatever the query, so dP - D must cancel: D of such rows comes from the same
+    # products as dP, and what is left is the weights' error (2^-18) of |dP|, not the output's rounding
+    lens = [1, 5, 1, 300, 2]
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32).cuda()
+    T, H = sum(lens), 2
+    q, k, v, dout = (x[0] for x in _inputs(1, T, T, H, H, D, 17, by=4.0))
+    plan = bfa.plan_blockids(cu_seqlens_q=cu, max_q=300, max_k=300)
+    shape = dict(softcap=cap, slopes=_slopes(H) if with_slopes else None)
+    out, lse = bfa.fwd(plan, q, k, v, **shape)
+    dq = bfa.bwd(plan, q, k, v, out, dout, lse, **shape)[0]
+    first = cu[:-1].long()
+    dp = (dout[first].double().abs() * v[first].double().abs()).sum(-1, keepdim=True)
+    bound = D ** -0.5 * k[first].double().abs() * dp * 2.0 ** -18
+    shaped.close(dq[first], torch.zeros_like(bound), bound + 1e-9, "dq of the first tokens")
