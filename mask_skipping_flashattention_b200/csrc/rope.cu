@@ -7,11 +7,12 @@
 // 1e-11 turns at position 10^6, where a product in fp32 would be off by 0.06
 // radians.
 //
-// Bound by HBM: two bytes in and two out a value.  A thread owns one chunk pair of a
-// head (two 16-byte chunks, 8 pairs) or one chunk that is copied, of one token, in every
-// kHeadLanes-th head: the trigonometry is paid once for all of them, neighbouring
-// threads cover kHeadLanes whole heads (1 KB at D 128), and kBatch heads are loaded before
-// the first is stored.
+// Bound by HBM: two bytes in and two out a value.  A block takes a few whole tokens:
+// their positions, then the cos and sin of every pair once into shared memory, then
+// all heads.  A thread owns one chunk pair of a head (two 16-byte chunks, 8 pairs) or
+// one chunk that is copied, in every kHeadLanes-th head: neighbouring threads cover
+// kHeadLanes whole heads (1 KB at D 128), and a batch of heads is loaded before the first is
+// stored.
 #include <cstdint>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -27,7 +28,8 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 constexpr int kHeadLanes = 4;
-constexpr int kBatch = 4;
+constexpr int kRopeTokens = 32;                 // most tokens of a block (8 threads a token at least)
+constexpr int kRopePairs = kRopeThreads / kHeadLanes * 8;  // most pairs of a block's tokens: 8 a chunk pair
 
 __device__ __forceinline__ float2 bf2_to_f2(uint32_t u) {
   return make_float2(__uint_as_float(u << 16), __uint_as_float(u & 0xffff0000u));
@@ -46,38 +48,65 @@ __device__ __forceinline__ int seq_of_token(const int32_t* cu, int n_seq, int64_
 
 }  // namespace
 
-// kRagged: positions and places from a ragged batch's lengths, keys and values into a cache
-template <bool kRagged>
-__global__ void __launch_bounds__(kRopeThreads) k_rope(const RopeParams p) {
-  const unsigned pairs = p.rotary / 16;                    // chunk pairs of a head that turn
-  const unsigned chunks = pairs + (p.D - p.rotary) / 8;    // and chunks that are copied
-  const unsigned lanes = chunks * kHeadLanes;              // threads of a token
-  const int64_t id = static_cast<int64_t>(blockIdx.x) * kRopeThreads + threadIdx.x;
-  const int64_t tok = id / lanes;
-  const unsigned in_tok = static_cast<unsigned>(id - tok * lanes);
-  const unsigned c = in_tok % chunks;
-  if (tok >= p.tokens) return;
-  const int64_t b = kRagged ? 0 : tok / p.S, st = tok - b * p.S;
+// kRagged: positions and places from a ragged batch's lengths, keys and values into a cache.
+// kBatch heads are in flight a thread: the ragged form, which waits longer for its start,
+// holds fewer so that more blocks are resident.
+template <bool kRagged, int kBatch>
+__global__ void __launch_bounds__(kRopeThreads, kRagged ? 4 : 3) k_rope(const RopeParams p) {
+  __shared__ int64_t pos_s[kRopeTokens], row_s[kRopeTokens];
+  __shared__ __align__(16) float2 turn_s[kRopePairs];     // (cos, sin) of a token's pairs, token-major
+  const unsigned pairs = p.rotary / 16;                   // chunk pairs of a head that turn
+  const unsigned chunks = pairs + (p.D - p.rotary) / 8;   // and chunks that are copied
+  const unsigned lanes = chunks * kHeadLanes;             // threads of a token
+  const unsigned per = p.tokens_per_block;
+  const int64_t tok0 = static_cast<int64_t>(blockIdx.x) * per;
 
-  // position of the token, and its place in the cache
-  int64_t pos;
-  int64_t row = -1;  // element offset of the token's cache row, or -1
-  if constexpr (!kRagged) {
-    const int64_t i = b * p.pos_sb + st;
-    pos = p.positions64 ? static_cast<const int64_t*>(p.positions)[i]
-                        : static_cast<int64_t>(static_cast<const int32_t*>(p.positions)[i]);
-  } else {
-    const int s = seq_of_token(p.cu_seqlens, p.n_seq, tok);
-    if (s >= p.n_seq) return;  // a row behind the last sequence
-    const int first = __ldg(p.cu_seqlens + s), end = __ldg(p.cu_seqlens + s + 1);
-    if (tok < first) return;
-    pos = static_cast<int64_t>(__ldg(p.seqused_k + s)) - (end - first) + (tok - first);
-    if (pos >= 0 && pos < static_cast<int64_t>(p.pages_per_seq) * p.page_size) {
-      const int pi = static_cast<int>(pos) / p.page_size;
-      const int64_t page = __ldg(p.block_table + static_cast<int64_t>(s) * p.pages_per_seq + pi);
-      if (page >= 0 && page < p.num_pages) row = page * p.c_sp + (static_cast<int>(pos) - pi * p.page_size) * p.c_st;
+  // position of each token, and its place in the cache: an element offset, -1 none, -2 not a token
+  if (threadIdx.x < per) {
+    const int64_t tok = tok0 + threadIdx.x;
+    int64_t pos = 0, row = -2;
+    if (tok < p.tokens) {
+      if constexpr (!kRagged) {
+        const int64_t b = tok / p.S, i = b * p.pos_sb + (tok - b * p.S);
+        pos = p.positions64 ? static_cast<const int64_t*>(p.positions)[i]
+                            : static_cast<int64_t>(static_cast<const int32_t*>(p.positions)[i]);
+        row = -1;
+      } else {
+        const int s = seq_of_token(p.cu_seqlens, p.n_seq, tok);
+        if (s < p.n_seq) {  // else a row behind the last sequence
+          const int first = __ldg(p.cu_seqlens + s), end = __ldg(p.cu_seqlens + s + 1);
+          if (tok >= first) {
+            row = -1;
+            pos = static_cast<int64_t>(__ldg(p.seqused_k + s)) - (end - first) + (tok - first);
+            if (pos >= 0 && pos < static_cast<int64_t>(p.pages_per_seq) * p.page_size) {
+              const int pi = static_cast<int>(pos) / p.page_size;
+              const int64_t page = __ldg(p.block_table + static_cast<int64_t>(s) * p.pages_per_seq + pi);
+              if (page >= 0 && page < p.num_pages)
+                row = page * p.c_sp + (static_cast<int>(pos) - pi * p.page_size) * p.c_st;
+            }
+          }
+        }
+      }
     }
+    pos_s[threadIdx.x] = pos;
+    row_s[threadIdx.x] = row;
   }
+  __syncthreads();
+  const unsigned half = p.rotary / 2;
+  for (unsigned i = threadIdx.x; i < per * half; i += kRopeThreads) {
+    const unsigned t = i / half;
+    // turns, minus the nearest integer: in [-1/2, 1/2]
+    const double x = static_cast<double>(pos_s[t]) * __ldg(p.inv_freq + (i - t * half)) * 0.15915494309189533577;
+    float sn, cs;
+    sincospif(2.f * static_cast<float>(x - rint(x)), &sn, &cs);
+    turn_s[i] = make_float2(cs * p.amplitude, sn * p.amplitude * p.sign);
+  }
+  __syncthreads();
+  const unsigned t = threadIdx.x / lanes, in_tok = threadIdx.x - t * lanes;
+  const unsigned c = in_tok % chunks;
+  if (t >= per || row_s[t] == -2) return;
+  const int64_t tok = tok0 + t, row = row_s[t];
+  const int64_t b = kRagged ? 0 : tok / p.S, st = tok - b * p.S;
 
   const bool turn = c < pairs;
   // element offsets of the thread's one or two chunks inside a head
@@ -87,14 +116,14 @@ __global__ void __launch_bounds__(kRopeThreads) k_rope(const RopeParams p) {
   else { ca = c * 8; cb = ca + p.rotary / 2; }
   float co[8], si[8];
   if (turn) {
+    const float4* v = reinterpret_cast<const float4*>(turn_s + t * half + c * 8);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      // turns, minus the nearest integer: in [-1/2, 1/2]
-      const double t = static_cast<double>(pos) * __ldg(p.inv_freq + c * 8 + i) * 0.15915494309189533577;
-      float sn, cs;
-      sincospif(2.f * static_cast<float>(t - rint(t)), &sn, &cs);
-      co[i] = cs * p.amplitude;
-      si[i] = sn * p.amplitude * p.sign;
+    for (int i = 0; i < 4; ++i) {
+      const float4 x = v[i];
+      co[2 * i] = x.x;
+      si[2 * i] = x.y;
+      co[2 * i + 1] = x.z;
+      si[2 * i + 1] = x.w;
     }
   }
 
@@ -164,20 +193,20 @@ cudaError_t launch_rope(const RopeParams& p0, int sms, cudaStream_t s) {
   const bool ragged = p.positions == nullptr;
   const int heads = p.H + 2 * p.Hkv;
   if (p.tokens <= 0 || heads <= 0) return cudaSuccess;
-  const int64_t threads = p.tokens * kHeadLanes * (p.rotary / 16 + (p.D - p.rotary) / 8);
-  // a block's share of the heads: all of them while that still gives every SM 2048
-  // threads, at least one batch round otherwise
+  const int lanes = kHeadLanes * (p.rotary / 16 + (p.D - p.rotary) / 8);  // 16 .. 64
+  p.tokens_per_block = kRopeThreads / lanes;
+  const int64_t blocks = (p.tokens + p.tokens_per_block - 1) / p.tokens_per_block;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  // a block's share of the heads: all of them while that still gives every SM 4 blocks
   const int rounds = (heads + kHeadLanes - 1) / kHeadLanes;
-  int64_t groups = (static_cast<int64_t>(sms) * 2048 + threads - 1) / threads;
+  int64_t groups = (static_cast<int64_t>(sms) * 4 + blocks - 1) / blocks;
   groups = groups < 1 ? 1 : (groups > rounds ? rounds : groups);
   p.heads_per_block = static_cast<int>((rounds + groups - 1) / groups) * kHeadLanes;
-  const int64_t blocks = (threads + kRopeThreads - 1) / kRopeThreads;
-  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   const unsigned gy = static_cast<unsigned>((heads + p.heads_per_block - 1) / p.heads_per_block);
   if (gy > 65535u) return cudaErrorInvalidConfiguration;
   const dim3 grid(static_cast<unsigned>(blocks), gy);
-  if (ragged) k_rope<true><<<grid, kRopeThreads, 0, s>>>(p);
-  else k_rope<false><<<grid, kRopeThreads, 0, s>>>(p);
+  if (ragged) k_rope<true, 2><<<grid, kRopeThreads, 0, s>>>(p);
+  else k_rope<false, 4><<<grid, kRopeThreads, 0, s>>>(p);
   return cudaGetLastError();
 }
 

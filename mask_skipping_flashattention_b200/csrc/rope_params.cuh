@@ -19,7 +19,7 @@ struct RopeParams {
   int64_t tokens;       // rows of q (batched: B * S)
   int32_t S;            // batched: tokens per batch row (packed: = tokens)
   int32_t H, Hkv;       // heads of q (0: none), of k and v (0: none)
-  int32_t heads_per_block;
+  int32_t heads_per_block, tokens_per_block;
   const __nv_bfloat16* q;
   int64_t q_sb, q_ss, q_sh;
   __nv_bfloat16* q_out;
