@@ -22,6 +22,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import math
 
 import numpy as np
@@ -88,7 +89,7 @@ def _run_on(t, stream, body):
     if not t.is_cuda:
         return body(0 if stream is None else _stream(stream), _keep)
     index = t.get_device()
-    if stream is None and index == torch.cuda.current_device():
+    if stream is None and index == torch._C._cuda_getDevice():
         return body(torch._C._cuda_getCurrentRawStream(index), _keep)
     with _launch_on(t, stream) as (st, finish):
         return body(st, finish)
@@ -115,15 +116,14 @@ def _strides_of(t):
 
 
 def _score_shape(softcap, slopes, q, H):
-    """(softcap or 0, contiguous slopes or None), checked."""
+    """softcap or 0; slopes checked."""
     if slopes is not None:
-        if slopes.dtype != torch.float32:
+        if slopes.dtype is not torch.float32:
             raise TypeError("slopes must be float32")
         if slopes.shape != (H,):
             raise ValueError(f"slopes must have one value per query head ({H}), not shape {tuple(slopes.shape)}")
         _same_device(q, slopes)
-        slopes = slopes.contiguous()
-    return float(softcap) if softcap is not None else 0.0, slopes
+    return float(softcap) if softcap is not None else 0.0
 
 
 def _ptr(t):
@@ -491,15 +491,16 @@ def _result(t, like_shape, dtype, device, name):
 def _fwd_shaped(plan, q, k, v, scale, out, return_lse, lse, stream, softcap, slopes):
     B, H, Hkv, D, lse_shape = _shapes(plan, q, k, v)
     _same_device(q, k, v)
-    cap, slopes = _score_shape(softcap, slopes, q, H)
+    cap = _score_shape(softcap, slopes, q, H)
     if lse is not None and return_lse and not lse.is_contiguous():
         raise ValueError("lse must be contiguous")
 
     def body(st, finish):
         o = _result(out, q.shape, torch.bfloat16, q.device, "out")
         l = _result(lse, lse_shape, torch.float32, q.device, "lse") if return_lse else None
+        sl = None if slopes is None else slopes.contiguous()
         _lib.check(_L.bfa_fwd_shaped(plan.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), _strides_of(q),
-                                     _strides_of(k), _strides_of(v), B, H, Hkv, D, scale or 0.0, cap, _addr(slopes),
+                                     _strides_of(k), _strides_of(v), B, H, Hkv, D, scale or 0.0, cap, _addr(sl),
                                      o.data_ptr(), _strides_of(o), _addr(l), st))
         finish(o if out is None else None, l if lse is None else None)
         return o, l
@@ -515,17 +516,18 @@ def _bwd_shaped(plan, q, k, v, out, dout, lse, scale, dq, dk, dv, stream, softca
     if lse is None or lse.dtype != torch.float32 or lse.shape != lse_shape:
         raise ValueError(f"lse (float32 {tuple(lse_shape)}, from fwd) is required")
     _same_device(q, k, v, out, dout, lse)
-    cap, slopes = _score_shape(softcap, slopes, q, H)
+    cap = _score_shape(softcap, slopes, q, H)
 
     def body(st, finish):
         gq = _result(dq, q.shape, torch.bfloat16, q.device, "dq")
         gk = _result(dk, k.shape, torch.bfloat16, q.device, "dk")
         gv = _result(dv, v.shape, torch.bfloat16, q.device, "dv")
         l = lse.contiguous()
+        sl = None if slopes is None else slopes.contiguous()
         _lib.check(_L.bfa_bwd_shaped(plan.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
                                      dout.data_ptr(), l.data_ptr(), _strides_of(q), _strides_of(k), _strides_of(v),
                                      _strides_of(out), _strides_of(dout), B, H, Hkv, D, scale or 0.0, cap,
-                                     _addr(slopes), gq.data_ptr(), gk.data_ptr(), gv.data_ptr(), _strides_of(gq),
+                                     _addr(sl), gq.data_ptr(), gk.data_ptr(), gv.data_ptr(), _strides_of(gq),
                                      _strides_of(gk), _strides_of(gv), st))
         finish(gq if dq is None else None, gk if dk is None else None, gv if dv is None else None)
         return gq, gk, gv
@@ -607,40 +609,48 @@ def fwd_paged(plan, q, k_cache, v_cache, block_table, scale=None, out=None, retu
 
 
 def _check_cache(k_cache, v_cache, block_table, cu_seqlens, seqused_k):
-    """(block_table, cu_seqlens, seqused_k) as contiguous int32, with the cache's form checked."""
-    if k_cache.dtype != torch.bfloat16 or v_cache.dtype != torch.bfloat16:
+    """The forms of a paged cache and a ragged batch's integers; (cache shape, cache strides)."""
+    if k_cache.dtype is not torch.bfloat16 or v_cache.dtype is not torch.bfloat16:
         raise TypeError("the caches must be bfloat16")
-    if k_cache.dim() != 4 or k_cache.stride() != v_cache.stride() or k_cache.shape != v_cache.shape:
+    shape, strides = k_cache.shape, k_cache.stride()
+    if len(shape) != 4 or strides != v_cache.stride() or shape != v_cache.shape:
         raise ValueError("k_cache and v_cache must be (num_pages, page_size, Hkv, D) with the same shape and strides")
-    if k_cache.stride(-1) != 1:
+    if strides[3] != 1:
         raise ValueError("the head dim of the caches must be contiguous")
-    B = seqused_k.numel()
-    if seqused_k.dim() != 1 or cu_seqlens.dim() != 1 or cu_seqlens.numel() != B + 1:
+    used = seqused_k.shape
+    if len(used) != 1 or cu_seqlens.shape != (used[0] + 1,):
         raise ValueError("cu_seqlens must hold one entry more than seqused_k")
-    if block_table.dim() != 2 or block_table.shape[0] != B:
+    table = block_table.shape
+    if len(table) != 2 or table[0] != used[0]:
         raise ValueError("block_table must be (sequences, pages per sequence)")
-    ints = []
-    for t, name in ((block_table, "block_table"), (cu_seqlens, "cu_seqlens"), (seqused_k, "seqused_k")):
-        if t.dtype not in (torch.int32, torch.int64):
-            raise TypeError(f"{name} must be int32 or int64")
-        ints.append(t if t.dtype is torch.int32 and t.is_contiguous() else t.to(torch.int32).contiguous())
-    _same_device(k_cache, v_cache, *ints)
-    return ints
+    for t in (block_table, cu_seqlens, seqused_k):
+        if t.dtype is not torch.int32 and t.dtype is not torch.int64:
+            raise TypeError("block_table, cu_seqlens and seqused_k must be int32 or int64")
+    _same_device(k_cache, v_cache, block_table, cu_seqlens, seqused_k)
+    # a cache of one page has no page stride of its own
+    return shape, _Strides3(strides[0] if shape[0] > 1 else shape[1] * strides[1], strides[1], strides[2])
+
+
+def _int32(t):
+    """t as contiguous int32; called where the launch's stream is current, since it may copy."""
+    return t if t.dtype is torch.int32 and t.is_contiguous() else t.to(torch.int32).contiguous()
+
+
+@functools.lru_cache(maxsize=1024)
+def _chunk_workspace(total_q, B, max_q, H, Hkv, D):
+    need = _L.bfa_fwd_chunk_workspace(total_q, B, max_q, H, Hkv, D)
+    if need < 0:
+        _lib.check(-2 if D not in (64, 128) else -1)
+    return need
 
 
 def _check_packed(t, name, heads, D):
-    if t.dtype != torch.bfloat16:
+    if t.dtype is not torch.bfloat16:
         raise TypeError(f"{name} must be bfloat16")
     if t.dim() != 3 or t.shape[2] != D or (heads is not None and t.shape[1] != heads):
         raise ValueError(f"{name} must be (tokens, {'heads' if heads is None else heads}, {D}), not {tuple(t.shape)}")
     if t.stride(-1) != 1:
         raise ValueError(f"the head dim of {name} must be contiguous")
-
-
-def _cache_strides(c):
-    # a cache of one page has no page stride of its own
-    st = c.stride()
-    return _Strides3(st[0] if c.shape[0] > 1 else c.shape[1] * st[1], st[1], st[2])
 
 
 def fwd_chunk(q, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, *, max_q=0, scale=None, window_left=-1,
@@ -658,29 +668,28 @@ def fwd_chunk(q, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, *, max_
     and a captured call follows their contents.  Rows of q behind the last sequence
     are left as they are in out and lse.
     """
-    table, cu, used = _check_cache(k_cache, v_cache, block_table, cu_seqlens_q, seqused_k)
-    num_pages, page_size, Hkv, D = k_cache.shape
+    (num_pages, page_size, Hkv, D), cache_strides = _check_cache(k_cache, v_cache, block_table, cu_seqlens_q, seqused_k)
     max_q, window_left = int(max_q), int(window_left)
     _check_packed(q, "q", None, D)
     _same_device(q, k_cache, workspace)
     T, H, _ = q.shape
-    B = used.numel()
-    cap, slopes = _score_shape(softcap, slopes, q, H)
-    need = _L.bfa_fwd_chunk_workspace(T, B, max_q, H, Hkv, D)
-    if need < 0:
-        _lib.check(-2 if D not in (64, 128) else -1)
+    B = seqused_k.shape[0]
+    cap = _score_shape(softcap, slopes, q, H)
+    need = _chunk_workspace(T, B, max_q, H, Hkv, D)
     if lse is not None and return_lse and not lse.is_contiguous():
         raise ValueError("lse must be contiguous")
 
     def body(st, finish):
+        table, cu, used = _int32(block_table), _int32(cu_seqlens_q), _int32(seqused_k)
+        sl = None if slopes is None else slopes.contiguous()
         o = _result(out, q.shape, torch.bfloat16, q.device, "out")
         l = _result(lse, (H, T), torch.float32, q.device, "lse") if return_lse else None
         ws = torch.empty(need, dtype=torch.uint8, device=q.device) if workspace is None else workspace
-        _lib.check(_L.bfa_fwd_chunk(q.data_ptr(), _strides_of(q), k_cache.data_ptr(), v_cache.data_ptr(),
-                                    _cache_strides(k_cache), num_pages, page_size, table.data_ptr(), table.shape[1],
-                                    cu.data_ptr(), used.data_ptr(), B, T, max_q, H, Hkv, D, scale or 0.0, window_left,
-                                    cap, _addr(slopes), o.data_ptr(), _strides_of(o), _addr(l), ws.data_ptr(),
-                                    ws.numel() * ws.element_size(), st))
+        _lib.check(_L.bfa_fwd_chunk(q.data_ptr(), _strides_of(q), k_cache.data_ptr(), v_cache.data_ptr(), cache_strides,
+                                    num_pages, page_size, table.data_ptr(), table.shape[1], cu.data_ptr(),
+                                    used.data_ptr(), B, T, max_q, H, Hkv, D, scale or 0.0, window_left, cap, _addr(sl),
+                                    o.data_ptr(), _strides_of(o), _addr(l), ws.data_ptr(),
+                                    need if workspace is None else ws.numel() * ws.element_size(), st))
         finish(o if out is None else None, l if lse is None else None)
         return o, l
 
@@ -718,12 +727,13 @@ def rope_frequencies(rotary, base=10000.0, *, factor=1.0, ramp=None, device="cud
 
 
 def _check_frequencies(inv_freq, like):
+    """rotary of the frequencies (0 without)."""
     if inv_freq is None:
-        return 0, None
-    if inv_freq.dtype != torch.float64 or inv_freq.dim() != 1:
+        return 0
+    if inv_freq.dtype is not torch.float64 or inv_freq.dim() != 1:
         raise TypeError("inv_freq must be a 1-D float64 tensor (rope_frequencies)")
     _same_device(like, inv_freq)
-    return 2 * inv_freq.numel(), inv_freq.contiguous()
+    return 2 * inv_freq.shape[0]
 
 
 def rope(x, positions, inv_freq, *, interleaved=False, amplitude=1.0, inverse=False, out=None, stream=None):
@@ -744,9 +754,8 @@ def rope(x, positions, inv_freq, *, interleaved=False, amplitude=1.0, inverse=Fa
     S, H, D = x.shape[-3:]
     if positions.shape not in ((S,), x.shape[:-2]):
         raise ValueError(f"positions must be {tuple(x.shape[:-2])} or {(S,)}, not {tuple(positions.shape)}")
-    rotary, inv_freq = _check_frequencies(inv_freq, x)
+    rotary = _check_frequencies(inv_freq, x)
     _same_device(x, positions)
-    positions = positions.contiguous()
     if out is not None and out.data_ptr() == x.data_ptr() and out.stride() != x.stride():
         raise ValueError("an in-place result must be x itself")
     if x.numel() == 0:
@@ -754,9 +763,9 @@ def rope(x, positions, inv_freq, *, interleaved=False, amplitude=1.0, inverse=Fa
 
     def body(st, finish):
         y = _result(out, x.shape, torch.bfloat16, x.device, "out")
-        _lib.check(_L.bfa_rope(x.data_ptr(), _strides_of(x), y.data_ptr(), _strides_of(y), positions.data_ptr(),
-                               1 if positions.dtype is torch.int64 else 0, S if positions.dim() == 2 else 0,
-                               _addr(inv_freq), rotary, B, S, H, D, 1 if interleaved else 0, amplitude,
+        at, f = positions.contiguous(), inv_freq.contiguous()
+        _lib.check(_L.bfa_rope(x.data_ptr(), _strides_of(x), y.data_ptr(), _strides_of(y), at.data_ptr(),
+                               1 if at.dtype is torch.int64 else 0, S if at.dim() == 2 else 0, f.data_ptr(), rotary, B, S, H, D, 1 if interleaved else 0, amplitude,
                                1 if inverse else 0, st))
         finish(y if out is None else None)
         return y
@@ -774,8 +783,7 @@ def append_paged(k, v, k_cache, v_cache, block_table, cu_seqlens, seqused_k, *, 
     ``inv_freq`` None: keys and queries are copied.  Rows behind the last sequence are left
     out.  Lengths and pages stay on the device, as for ``fwd_chunk``.
     """
-    table, cu, used = _check_cache(k_cache, v_cache, block_table, cu_seqlens, seqused_k)
-    num_pages, page_size, Hkv, D = k_cache.shape
+    (num_pages, page_size, Hkv, D), cache_strides = _check_cache(k_cache, v_cache, block_table, cu_seqlens, seqused_k)
     _check_packed(k, "k", Hkv, D)
     _check_packed(v, "v", Hkv, D)
     T, H = k.shape[0], Hkv
@@ -791,16 +799,18 @@ def append_paged(k, v, k_cache, v_cache, block_table, cu_seqlens, seqused_k, *, 
             raise ValueError("an in-place q_out must be q itself")
     elif q_out is not None:
         raise ValueError("q_out without q")
-    rotary, inv_freq = _check_frequencies(inv_freq, k)
+    rotary = _check_frequencies(inv_freq, k)
 
     def body(st, finish):
         qo = None if q is None else _result(q_out, q.shape, torch.bfloat16, q.device, "q_out")
         none3 = _Strides3(0, 0, 0)
+        table, cu, used = _int32(block_table), _int32(cu_seqlens), _int32(seqused_k)
+        f = None if inv_freq is None else inv_freq.contiguous()
         _lib.check(_L.bfa_append_paged(k.data_ptr(), _strides_of(k), v.data_ptr(), _strides_of(v), _addr(q),
                                        none3 if q is None else _strides_of(q), _addr(qo),
                                        none3 if q is None else _strides_of(qo), k_cache.data_ptr(), v_cache.data_ptr(),
-                                       _cache_strides(k_cache), num_pages, page_size, table.data_ptr(), table.shape[1],
-                                       cu.data_ptr(), used.data_ptr(), used.numel(), T, H, Hkv, D, _addr(inv_freq),
+                                       cache_strides, num_pages, page_size, table.data_ptr(), table.shape[1],
+                                       cu.data_ptr(), used.data_ptr(), used.shape[0], T, H, Hkv, D, _addr(f),
                                        rotary, 1 if interleaved else 0, amplitude, st))
         finish(qo if q_out is None else None)
         return qo

@@ -289,3 +289,24 @@ def test_a_short_wait_bound_is_reported_and_leaves_nothing_behind():
     got = b.call()
     bfa.chunk_device_status()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def test_other_integer_types_and_strides_on_another_stream():
+    # they are copied where the launch's stream is current, behind what that stream has queued
+    b = Batch([1, 70], [200, 333], 8, 2, 64, 16)
+    slopes = torch.stack((_slopes(8), _slopes(8)), 1)[:, 0]
+    want = b.call(slopes=slopes)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        table, cu, used = b.table.long() + 0, b.cu.long() + 0, b.used.long() + 0
+    wide = torch.stack((table, table), 2)[:, :, 0]
+    side.wait_stream(torch.cuda.current_stream())
+    got = bfa.fwd_chunk(b.q, b.k_cache, b.v_cache, wide, cu, used, max_q=70, slopes=slopes, stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    # the raw handle of a stream, too
+    raw = bfa.fwd_chunk(b.q, b.k_cache, b.v_cache, b.table, b.cu, b.used, max_q=70, slopes=slopes,
+                        stream=side.cuda_stream)
+    torch.cuda.synchronize()
+    assert torch.equal(raw[0], want[0])

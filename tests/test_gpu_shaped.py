@@ -276,3 +276,18 @@ def test_a_row_with_a_single_key_has_no_query_gradient(D, cap, with_slopes):
     dp = (dout[first].double().abs() * v[first].double().abs()).sum(-1, keepdim=True)
     bound = D ** -0.5 * k[first].double().abs() * dp * 2.0 ** -18
     shaped.close(dq[first], torch.zeros_like(bound), bound + 1e-9, "dq of the first tokens")
+
+
+def test_repeated_data_is_refused():
+    # an expanded tensor has a stride of 0, which the tensor maps cannot hold
+    S, H, D = 130, 4, 64
+    q, k, v, dout = _inputs(2, S, S, H, H, D, 131)
+    plan = bfa.plan_blockids(B=2, Sq=S, Sk=S)
+    out, lse = bfa.fwd(plan, q, k, v, softcap=9.0)
+    for bad in (k[:, :, :1].expand(2, S, H, D), k[:1].expand(2, S, H, D), k[:, :1].expand(2, S, H, D)):
+        with pytest.raises(bfa.BfaError) as e:
+            bfa.fwd(plan, q, bad, v, softcap=9.0)
+        assert e.value.status == "BFA_ERR_UNSUPPORTED"
+    with pytest.raises(bfa.BfaError) as e:
+        bfa.bwd(plan, q, k, v, out, dout[:, :1].expand(2, S, H, D), lse, softcap=9.0)
+    assert e.value.status == "BFA_ERR_UNSUPPORTED"

@@ -107,9 +107,12 @@ def test_chunk_refuses_other_caches():
             bfa.fwd_chunk(q, kc, vc, bt, CU, USED, stream=0)
 
 
-def test_chunk_workspace_grows_with_the_call():
+def test_chunk_workspace_sizes():
     size = lambda *a: bfa._L.bfa_fwd_chunk_workspace(*a)  # noqa: E731
-    assert 0 < size(1, 1, 1, 32, 8, 128) < size(64, 64, 1, 32, 8, 128)
+    # few rows need the row kernel's places, more of them the tile kernel's, a mixed batch both
+    one, long, mixed = size(1, 1, 1, 32, 8, 128), size(600, 1, 600, 32, 8, 128), size(600, 2, 600, 32, 8, 128)
+    assert 0 < one < long < mixed and mixed == one + long and size(64, 64, 1, 32, 8, 128) == one
+    assert size(600, 1, 0, 32, 8, 128) == long  # an unknown max_q is the longest it can be
     assert size(1, 1, 1, 32, 8, 96) == -1 and size(1, 1, 1, 30, 8, 64) == -1 and size(-1, 1, 1, 8, 8, 64) == -1
 
 
