@@ -1624,15 +1624,15 @@ ChunkSplit chunk_split(int64_t total_q, int64_t B, int64_t max_q, int H, int Hkv
   if (!few) {
     c.tile.rows = kChunkTileRows;
     c.tile.slots = sm_count();
-    c.tile.min_share = 4;
-    c.tile.start_cost = 2;
+    c.tile.min_share = 2;
+    c.tile.start_cost = 4;
     c.tile.bytes = part_bytes(c.tile.slots, c.tile.rows, D);
   }
   if (few || (B > 1 && G <= kChunkRows)) {  // one sequence alone goes to the tile kernel whatever its length
     c.row.rows = kChunkRows;
     c.row.slots = 2 * sm_count();
-    c.row.min_share = 4;
-    c.row.start_cost = 2;
+    c.row.min_share = 2;
+    c.row.start_cost = 4;
     c.row.bytes = part_bytes(c.row.slots, c.row.rows, D);
   }
   return c;

@@ -338,10 +338,11 @@ __global__ void __launch_bounds__(kRowThreads, 2) k_chunk_rows(const ChunkParams
 // Join the pieces of the cut units: out = sum_i 2^(m_i - M) o_i / sum_i 2^(m_i - M) l_i.
 // A unit of P pieces has P - 1 cuts, and each takes its share of the unit's rows (so
 // every cut has about as much to join); `part` of `parts` blocks of a cut takes some of
-// those.  Few pieces: a warp a row.  Many (a long sequence has hundreds): the
-// block's warps share the pieces of a row, since one after the other their latencies
-// would add up.  The order of the sums depends on the number of pieces alone.
-constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps, kJoinFew = 8;
+// those.  It is all latency, so rows or pieces go side by side: four rows a warp at up to
+// four pieces, a row a warp at up to 32 (lane i holds piece i's maximum), and beyond
+// (a long sequence has hundreds) the block's warps share the pieces of a row.  The order
+// of the sums depends on the number of pieces alone.
+constexpr int kJoinWarps = 8, kJoinThreads = 32 * kJoinWarps;
 
 template <int D>
 struct JoinShared {
@@ -379,28 +380,65 @@ __device__ __forceinline__ void join_cut(const ChunkParams& p, int cut, int part
       *dst = pack_bf16x2(o[0] * inv, o[1] * inv);
     if (p.lse && lane == 0) p.lse[static_cast<int64_t>(h) * p.total_q + tok] = lse_of(M, L);
   };
-  if (c.pieces <= kJoinFew) {
-    for (int r = ra + part * kJoinWarps + warp; r < rb; r += parts * kJoinWarps) {
-      // lane i holds piece i's maximum and sum; a piece that saw no key of this row left zeros
-      const float2 ml = lane < c.pieces ? p.ws_ml[place(lane, r)] : make_float2(-INFINITY, 0.f);
-      float a[kJoinFew][kV];
+  if (c.pieces <= 4) {
+    for (int r4 = ra + (part * kJoinWarps + warp) * 4; r4 < rb; r4 += parts * kJoinWarps * 4) {
+      // lane 8 r + i holds the maximum and sum of row r4 + r, piece i; a piece that saw no key
+      // of a row left zeros
+      const int lr = lane >> 3, li = lane & 7;
+      const bool in = r4 + lr < rb && li < c.pieces;
+      const float2 ml = in ? p.ws_ml[place(li, r4 + lr)] : make_float2(-INFINITY, 0.f);
+      float a[4][4][kV];
 #pragma unroll
-      for (int i = 0; i < kJoinFew; ++i)
-        if (i < c.pieces) load(place(i, r), a[i]);
+      for (int r = 0; r < 4; ++r)
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (r4 + r < rb && i < c.pieces) load(place(i, r4 + r), a[r][i]);
       float M = ml.x;
 #pragma unroll
       for (int d = 4; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
-      M = __shfl_sync(0xffffffffu, M, 0);
       const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
-      float o[kV] = {}, L = 0.f;
 #pragma unroll
-      for (int i = 0; i < kJoinFew; ++i)
-        if (i < c.pieces) {
-          const float fi = __shfl_sync(0xffffffffu, f, i);
-          L = fmaf(__shfl_sync(0xffffffffu, ml.y, i), fi, L);
+      for (int r = 0; r < 4; ++r) {
+        float o[kV] = {}, L = 0.f;
 #pragma unroll
-          for (int v = 0; v < kV; ++v) o[v] = fmaf(a[i][v], fi, o[v]);
+        for (int i = 0; i < 4; ++i) {
+          const float fi = __shfl_sync(0xffffffffu, f, 8 * r + i);
+          L = fmaf(__shfl_sync(0xffffffffu, ml.y, 8 * r + i), fi, L);
+          if (r4 + r < rb && i < c.pieces) {
+#pragma unroll
+            for (int v = 0; v < kV; ++v) o[v] = fmaf(a[r][i][v], fi, o[v]);
+          }
         }
+        const float Mr = __shfl_sync(0xffffffffu, M, 8 * r);
+        if (r4 + r < rb) store(r4 + r, o, Mr, L);
+      }
+    }
+    return;
+  }
+  if (c.pieces <= 32) {
+    constexpr int kSide = 8;
+    for (int r = ra + part * kJoinWarps + warp; r < rb; r += parts * kJoinWarps) {
+      const float2 ml = lane < c.pieces ? p.ws_ml[place(lane, r)] : make_float2(-INFINITY, 0.f);
+      float o[kV] = {}, L = 0.f, M = ml.x;
+#pragma unroll
+      for (int d = 16; d > 0; d >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, d));
+      const float f = ml.x == -INFINITY ? 0.f : ex2_approx(ml.x - M);
+      for (int i0 = 0; i0 < c.pieces; i0 += kSide) {
+        float a[kSide][kV];
+#pragma unroll
+        for (int i = 0; i < kSide; ++i)
+          if (i0 + i < c.pieces) load(place(i0 + i, r), a[i]);
+#pragma unroll
+        for (int i = 0; i < kSide; ++i) {
+          const float fi = __shfl_sync(0xffffffffu, f, (i0 + i) & 31);
+          const float li = __shfl_sync(0xffffffffu, ml.y, (i0 + i) & 31);
+          if (i0 + i < c.pieces) {
+            L = fmaf(li, fi, L);
+#pragma unroll
+            for (int v = 0; v < kV; ++v) o[v] = fmaf(a[i][v], fi, o[v]);
+          }
+        }
+      }
       store(r, o, M, L);
     }
     return;

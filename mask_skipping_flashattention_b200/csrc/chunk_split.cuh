@@ -68,9 +68,10 @@ __device__ __forceinline__ SeqSpan seq_span(const ChunkParams& p, int s) {
 // length of the line before row tile rt of a sequence's kv head
 template <int R, int T>
 __device__ __forceinline__ int64_t line_before(const ChunkParams& p, const SeqSpan& sp, unsigned rt) {
-  const unsigned reach = p.window >= 0 ? min(sp.kv, p.window + sp.q_len) : sp.kv;  // keys of the whole chunk
-  if (R == kChunkRows || p.window >= 0)  // every unit alike
+  if (R == kChunkRows || p.window >= 0) {  // every unit alike: the window and its own tokens, or all keys
+    const unsigned reach = p.window >= 0 ? min(sp.kv, p.window + min(sp.q_len, R / p.G + 1)) : sp.kv;
     return static_cast<int64_t>(rt) * (reach / T + 1 + p.start_cost);
+  }
   // causal: unit i sees the keys before the chunk and R (i + 1) / G tokens of it (R = 2 T;
   // row tiles stay below 2^15)
   const unsigned before = max(sp.kv - sp.q_len, 0);

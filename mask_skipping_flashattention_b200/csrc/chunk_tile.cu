@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __shared__ __align__(8) uint64_t bars[NBAR];
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
-  __shared__ TileWork wk_s;
+  __shared__ TileWork wk_s[2];  // this piece and the next one
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   auto bar = [&](int i) { return smem_u32(&bars[i]); };
@@ -83,41 +83,39 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
 
   grid_trigger();  // the row kernel, or the join, may take the place of blocks that are done
-  // warp 0 walks this block's share of the line
+  // warp 3 walks this block's share of the line, a piece ahead of the others
   Walk walk;
   int64_t left = 0;
   bool more = false;
-  if (warp == 0) {
+  auto post_piece = [&](TileWork& w) {
+    if (more) {
+      const int64_t x1 = min(walk.w, walk.x + left);
+      const Piece pc = piece_of<kUnitRows, kTile>(p, walk, x1, blockIdx.x);
+      left -= x1 - walk.x;
+      if (lane == 0) {
+        w.pc = pc;
+        w.rows = pc.sp.q_len * p.G;
+        w.row0 = pc.rt * kUnitRows;
+        w.n = pc.t1 - pc.t0;
+        w.two = pc.rt * kUnitRows + kTile < pc.sp.q_len * p.G;
+      }
+    }
+    if (lane == 0) w.have = more;
+    more = more && left > 0 && walk.template next<kUnitRows, kTile>(p);
+  };
+  if (warp == 3) {
     const Line ln = line_of<kUnitRows, kTile>(p);
     const int64_t pos = ln.share * blockIdx.x;
     left = min(ln.share, ln.total - pos);
     more = left > 0;
     if (more) walk = walk_to<kUnitRows, kTile>(p, pos);
     if (lane == 0) note_cut(p, walk, ln.share, blockIdx.x, more);
+    post_piece(wk_s[0]);
   }
-  auto post_piece = [&]() {  // warp 0
-    if (more) {
-      const int64_t x1 = min(walk.w, walk.x + left);
-      const Piece pc = piece_of<kUnitRows, kTile>(p, walk, x1, blockIdx.x);
-      left -= x1 - walk.x;
-      if (lane == 0) {
-        wk_s.pc = pc;
-        wk_s.rows = pc.sp.q_len * p.G;
-        wk_s.row0 = pc.rt * kUnitRows;
-        wk_s.n = pc.t1 - pc.t0;
-        wk_s.two = pc.rt * kUnitRows + kTile < pc.sp.q_len * p.G;
-      }
-    }
-    if (lane == 0) wk_s.have = more;
-    more = more && left > 0 && walk.template next<kUnitRows, kTile>(p);
-  };
-  if (warp == 0) {
-    if (lane == 0) {
-      abort_flag = 0;
-      for (int i = 0; i < NBAR; ++i) mbar_init(bar(i), i == BQ ? 9 : ((i == BP || i == BP + 1) ? 4 : 1));
-      fence_barrier_init();
-    }
-    post_piece();
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int i = 0; i < NBAR; ++i) mbar_init(bar(i), i == BQ ? 9 : ((i == BP || i == BP + 1) ? 4 : 1));
+    fence_barrier_init();
   }
   if (warp == 1) {
     tmem_alloc(smem_u32(&tmem_slot), C::kTmemCols);
@@ -125,22 +123,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   meet();
   const uint32_t tmem = tmem_slot;
-  const TileWork& wk = wk_s;
   const uint64_t cap = p.wait_ns;
   // what the barriers have seen before this piece: pieces with tiles, tiles (F), commits of E,
   // tiles of each slot, edge tiles.  Every role counts for itself, all alike.
   int c_piece = 0, c_f = 0, c_e = 0, c_s1 = 0, c_z = 0;
-  auto count_piece = [&](int n) {
+  int cur = 0;  // this piece's half of wk_s
+  auto count_piece = [&](int n, int two) {
     if (n > 0) {
       ++c_piece;
       c_f += n;
       c_e += n + 1;
-      c_s1 += wk.two ? n : 0;
+      c_s1 += two ? n : 0;
     }
+    cur ^= 1;
   };
 
   // a tile with value rows that no row of the unit may read
-  auto edge = [&](int j) {
+  auto edge = [&](const TileWork& wk, int j) {
     const int k0 = (wk.pc.t0 + j) * kTile;
     return k0 < wk.pc.lo || k0 + kTile > wk.pc.hi;
   };
@@ -148,8 +147,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (warp < 4) {
     // ============================================================ warpgroup 0
     regs_dec<kRegsWG0>();
-    while (wk.have) {
-      const int n = wk.n;
+    while (wk_s[cur].have) {
+      const TileWork& wk = wk_s[cur];
+      const int n = wk.n, two_slots = wk.two;
+      if (warp == 3) post_piece(wk_s[cur ^ 1]);
       if (warp == 0 && n > 0) {
         // -------------------------------------------------------- producer
         // K of the first tile on BQ; at step j, V of tile j and K of tile j + 1 on the
@@ -228,7 +229,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int f = c_f + u, st = f & 1, st1 = st ^ 1;
           const bool have_next = u + 1 < n;
           if (!mbar_wait_fast(bar(BF + st), (f >> 1) & 1, cap, &abort_flag)) { ok = false; break; }
-          if (edge(u)) {
+          if (edge(wk, u)) {
             mbar_arrive(bar(BY));
             if (!mbar_wait_fast(bar(BZ), z & 1, cap, &abort_flag)) { ok = false; break; }
             ++z;
@@ -259,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       } else if (warp == 2 && n > 0) {
         // -------------------------------------------------------- value rows outside the unit's keys
         for (int j = 0; j < n; ++j) {
-          if (!edge(j)) continue;
+          if (!edge(wk, j)) continue;
           // the MMA thread waits at this tile, so its stage's phase cannot move on
           const int f = c_f + j;
           bool got = mbar_wait(bar(BY), c_z & 1, cap, &abort_flag);
@@ -280,10 +281,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
       }
       __syncwarp();
-      count_piece(n);
+      count_piece(n, two_slots);
       meet();
-      if (*static_cast<volatile int*>(&abort_flag)) break;  // set before the barrier: the same for every thread
-      if (warp == 0) post_piece();
+      if (*static_cast<volatile int*>(&abort_flag)) break;  // waits are over: the same for every thread
       meet();
     }
   } else {
@@ -295,8 +295,9 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem_addr(tmem + (slot ? C::kColS1 : C::kColS0), quarter * 32, 0);
     const uint32_t tO = tmem_addr(tmem + (slot ? C::kColO1 : C::kColO0), quarter * 32, 0);
     const uint32_t barS = bar(BS + slot), barP = bar(BP + slot);
-    while (wk.have) {
-      const int n = wk.n;
+    while (wk_s[cur].have) {
+      const TileWork& wk = wk_s[cur];
+      const int n = wk.n, two_slots = wk.two;
       const int r = wk.row0 + slot * kTile + row;  // row of the chunk: token r / G, head r % G
       const bool valid = r < wk.rows;
       const int q_len = wk.pc.sp.q_len, kv = wk.pc.sp.kv;
@@ -446,7 +447,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
         }
       }
-      count_piece(n);
+      count_piece(n, two_slots);
       meet();
       if (*static_cast<volatile int*>(&abort_flag)) break;
       meet();
