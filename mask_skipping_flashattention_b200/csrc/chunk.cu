@@ -360,12 +360,15 @@ __device__ __forceinline__ void join_cut(const ChunkParams& p, int cut, int part
   const int first = cut - 1 - c.index;  // the block that starts the unit (its odd place); the others' even ones
   const int ra = n * c.index / cuts, rb = n * (c.index + 1) / cuts;
   auto place = [&](int i, int r) { return static_cast<int64_t>(i == 0 ? 2 * first + 1 : 2 * (first + i)) * R + r; };
+  // the lane's columns of a workspace row; the tile kernel's rows have their 16-byte chunks
+  // swizzled by the row's place among 32
   auto load = [&](int64_t at, float (&a)[kV]) {
+    const int mix = R == kChunkTileRows ? static_cast<int>(at) & (D / 4 - 1) & 31 : 0;
     if constexpr (kV == 4) {
-      const float4 v = *reinterpret_cast<const float4*>(p.ws_o + at * D + lane * 4);
+      const float4 v = *reinterpret_cast<const float4*>(p.ws_o + at * D + (lane ^ mix) * 4);
       a[0] = v.x; a[1] = v.y; a[2] = v.z; a[3] = v.w;
     } else {
-      const float2 v = *reinterpret_cast<const float2*>(p.ws_o + at * D + lane * 2);
+      const float2 v = *reinterpret_cast<const float2*>(p.ws_o + at * D + (((lane >> 1) ^ mix) << 2) + (lane & 1) * 2);
       a[0] = v.x; a[1] = v.y;
     }
   };

@@ -308,14 +308,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int hi = valid ? min(kv, pos + 1) : 0x7fffffff;
       const int lo = valid && p.window >= 0 ? max(0, pos - p.window + 1) : 0;
       if (n > 0) {
-        // this thread's row of Q into the swizzled tile (K-major operand of S)
-        const uint4* src = reinterpret_cast<const uint4*>(p.q + (static_cast<int64_t>(wk.pc.sp.q0) + tok) * p.q_ss +
-                                                          static_cast<int64_t>(h) * p.q_sh);
-        const uint32_t dst = smem_u32(slot ? sQ1 : sQ0) + row * 128;
+        // The warp's 32 rows of Q into the swizzled tile (K-major operand of S), whole rows
+        // at a time: a row a thread would touch 32 lines an instruction.
+        constexpr int kChunks = D / 8, kPer = 32 / kChunks;  // 16-byte chunks of a row, rows an instruction
+        const uint32_t tile = smem_u32(slot ? sQ1 : sQ0);
+        const int c16 = lane % kChunks;
+        const __nv_bfloat16* src = p.q + (static_cast<int64_t>(wk.pc.sp.q0) + tok) * p.q_ss + static_cast<int64_t>(h) * p.q_sh;
+        const uint64_t at = valid ? reinterpret_cast<uint64_t>(src) : 0;  // of this lane's row
 #pragma unroll
-        for (int c16 = 0; c16 < D / 8; ++c16) {
-          const uint4 v = valid ? src[c16] : make_uint4(0u, 0u, 0u, 0u);
-          st_shared_v4(dst + (c16 >> 3) * 16384 + (((c16 & 7) ^ (row & 7)) << 4), v.x, v.y, v.z, v.w);
+        for (int half = 0; half < 2; ++half) {
+          uint4 v[16 / kPer];
+#pragma unroll
+          for (int i = 0; i < 16 / kPer; ++i) {
+            const uint64_t row_at = __shfl_sync(0xffffffffu, at, half * 16 + i * kPer + lane / kChunks);
+            v[i] = row_at ? *(reinterpret_cast<const uint4*>(row_at) + c16) : make_uint4(0u, 0u, 0u, 0u);
+          }
+#pragma unroll
+          for (int i = 0; i < 16 / kPer; ++i) {
+            const int tr = quarter * 32 + half * 16 + i * kPer + lane / kChunks;
+            st_shared_v4(tile + (c16 >> 3) * 16384 + tr * 128 + (((c16 & 7) ^ (tr & 7)) << 4), v[i].x, v[i].y, v[i].z,
+                         v[i].w);
+          }
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -407,11 +420,17 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_after();
         if (ok) {
+          // The rows leave through shared memory (every product is done, so all of it but the
+          // other warps' parts is free), 16-byte chunks swizzled by the row so that neither
+          // side meets in a bank.  Direct stores, a row a thread, took 5 us.
           const bool whole = wk.pc.whole != 0;
           const float inv = l > 0.f ? 1.f / l : 0.f;
           const int64_t gtok = static_cast<int64_t>(wk.pc.sp.q0) + tok;
           const int64_t wr = static_cast<int64_t>(wk.pc.place) * kUnitRows + slot * kTile + row;
-          __nv_bfloat16* op = p.out + gtok * p.o_ss + static_cast<int64_t>(h) * p.o_sh;
+          // this warp's 32 rows: bf16 in the slot's Q tile, fp32 in a K or V stage pair
+          constexpr int kWide = D / 4;  // 16-byte chunks of an fp32 row
+          const uint32_t stg = whole ? smem_u32(slot ? sQ1 : sQ0) + quarter * 32 * D * 2
+                                     : smem_u32(sK0) + (slot * kTile + quarter * 32) * D * 4;
 #pragma unroll 1
           for (int cc = 0; cc < D / 32; ++cc) {
             uint32_t o[32];
@@ -423,27 +442,48 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int j = 0; j < 32; ++j) o[j] = 0u;
             }
-            if (valid && whole) {
+            if (whole) {
 #pragma unroll
               for (int j = 0; j < 4; ++j) {
                 uint32_t w[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
                   w[e] = pack_bf16x2(__uint_as_float(o[8 * j + 2 * e]) * inv, __uint_as_float(o[8 * j + 2 * e + 1]) * inv);
-                reinterpret_cast<uint4*>(op + cc * 32)[j] = make_uint4(w[0], w[1], w[2], w[3]);
+                st_shared_v4(stg + lane * D * 2 + (((cc * 4 + j) ^ (lane & (D / 8 - 1))) << 4), w[0], w[1], w[2], w[3]);
               }
-            } else if (valid) {
-              uint4* d4 = reinterpret_cast<uint4*>(p.ws_o + wr * D + cc * 32);
+            } else {
 #pragma unroll
-              for (int j = 0; j < 8; ++j) d4[j] = make_uint4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+              for (int j = 0; j < 8; ++j)
+                st_shared_v4(stg + lane * D * 4 + (((cc * 8 + j) ^ (lane & (kWide - 1))) << 4), o[4 * j], o[4 * j + 1],
+                             o[4 * j + 2], o[4 * j + 3]);
             }
           }
-          if (valid && whole) {
-            if (p.lse)
+          if (whole) {
+            __syncwarp();
+            constexpr int kChunks = D / 8, kPer = 32 / kChunks;
+            const int c16 = lane % kChunks;
+            const uint64_t at = valid ? reinterpret_cast<uint64_t>(p.out + gtok * p.o_ss + static_cast<int64_t>(h) * p.o_sh) : 0;
+#pragma unroll 8
+            for (int i = 0; i < 32 / kPer; ++i) {
+              const int wrow = i * kPer + lane / kChunks;
+              const uint64_t row_at = __shfl_sync(0xffffffffu, at, wrow);
+              const float4 v = ld_shared_f4(stg + wrow * D * 2 + ((c16 ^ (wrow & (kChunks - 1))) << 4));
+              if (row_at) *(reinterpret_cast<float4*>(row_at) + c16) = v;
+            }
+            if (valid && p.lse)
               p.lse[static_cast<int64_t>(h) * p.total_q + gtok] =
                   l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
-          } else if (valid) {
+          } else {
+            // the swizzled rows go to the workspace as they are (the join undoes it)
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              bulk_store(p.ws_o + (wr - row + quarter * 32) * D, stg, 32 * D * 4);
+              bulk_commit_group();
+            }
             p.ws_ml[wr] = make_float2(m, l);
+            if (lane == 0) bulk_wait_group_read0();  // the stages are the next piece's
+            __syncwarp();
           }
         }
       }
@@ -455,6 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 
   // ------------------------------------------------------------ teardown
+  bulk_wait_group0();  // the workspace is written before the join may read it
   tc_fence_before();
   __syncthreads();
   if (abort_flag && threadIdx.x == 0) atomicOr(p.err, DEVERR_TIMEOUT);
