@@ -1569,8 +1569,8 @@ bfa_status check_heads(int H, int Hkv, int D) {
 }
 
 // caches, page table and lengths of a ragged batch (the forms of bfa_fwd_paged)
-bfa_status check_cache(const void* k_cache, const void* v_cache, const int64_t* cs, int64_t num_pages, int page_size,
-                       const int32_t* block_table, int pages_per_seq, const int32_t* cu_seqlens,
+bfa_status check_cache(const void* k_cache, const void* v_cache, const int64_t* cs, int Hkv, int64_t num_pages,
+                       int page_size, const int32_t* block_table, int pages_per_seq, const int32_t* cu_seqlens,
                        const int32_t* seqused_k, int B, int64_t total) {
   if (!(page_size == 8 || page_size == 16 || page_size == 32 || page_size == 64 ||
         (page_size > 0 && page_size % kTile == 0)))
@@ -1590,7 +1590,7 @@ bfa_status check_cache(const void* k_cache, const void* v_cache, const int64_t* 
     return s;
   if (cs[0] != static_cast<int64_t>(page_size) * cs[1])
     return fail(BFA_ERR_INVALID_ARG, "cache pages must be contiguous (page stride = page_size * token stride)");
-  if (cs[1] == 0 || cs[2] == 0)
+  if (cs[1] == 0 || (cs[2] == 0 && Hkv > 1))
     return fail(BFA_ERR_INVALID_ARG, "the caches' token and head strides must be positive");
   return BFA_OK;
 }
@@ -1679,7 +1679,7 @@ BFA_API bfa_status bfa_fwd_chunk(const void* q, const int64_t qs[3], const void*
   if ((s = check_heads(H, Hkv, D)) || (s = check_softcap(softcap))) return s;
   if (window_left == 0 || window_left < -1)
     return fail(BFA_ERR_INVALID_ARG, "window_left=%d must be positive, or -1 for no window", window_left);
-  if ((s = check_cache(k_cache, v_cache, cs, num_pages, page_size, block_table, pages_per_seq, cu_seqlens_q, seqused_k,
+  if ((s = check_cache(k_cache, v_cache, cs, Hkv, num_pages, page_size, block_table, pages_per_seq, cu_seqlens_q, seqused_k,
                        B, total_q)))
     return s;
   if (total_q == 0) return BFA_OK;
@@ -1841,7 +1841,7 @@ BFA_API bfa_status bfa_append_paged(const void* k, const int64_t ks[3], const vo
                                     float amplitude, void* stream) {
   bfa_status s;
   if ((s = check_heads(q ? H : Hkv, Hkv, D)) ||
-      (s = check_cache(k_cache, v_cache, cs, num_pages, page_size, block_table, pages_per_seq, cu_seqlens, seqused_k, B,
+      (s = check_cache(k_cache, v_cache, cs, Hkv, num_pages, page_size, block_table, pages_per_seq, cu_seqlens, seqused_k, B,
                        total)) ||
       (s = check_rotary(inv_freq, rotary, D, amplitude, true)))
     return s;

@@ -1,5 +1,9 @@
 """Attention of new tokens over a paged cache, against the 64-bit form of tests/shaped.py."""
 
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -7,6 +11,8 @@ import torch
 import shaped
 
 pytestmark = pytest.mark.gpu
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 bfa = pytest.importorskip("mask_skipping_flashattention_b200")
 
@@ -310,3 +316,49 @@ def test_other_integer_types_and_strides_on_another_stream():
                         stream=side.cuda_stream)
     torch.cuda.synchronize()
     assert torch.equal(raw[0], want[0])
+
+
+FIRST_CALLS = """
+import torch
+import mask_skipping_flashattention_b200 as bfa
+BF = torch.bfloat16
+g = torch.Generator(device="cuda").manual_seed(1)
+r = lambda *s: torch.randn(*s, generator=g, device="cuda").to(BF)
+kc, vc, q, k, v = r(40, 16, 2, 64), r(40, 16, 2, 64), r(101, 8, 64), r(101, 2, 64), r(101, 2, 64)
+table = torch.arange(40, dtype=torch.int32, device="cuda").reshape(2, 20)
+cu = torch.tensor([0, 1, 101], dtype=torch.int32, device="cuda")
+used = torch.tensor([200, 300], dtype=torch.int32, device="cuda")
+f = torch.pow(100.0, -torch.arange(32, dtype=torch.float64, device="cuda"))
+p = torch.arange(101, dtype=torch.int32, device="cuda")
+
+def step():
+    qr = bfa.append_paged(k, v, kc, vc, table, cu, used, q=q, inv_freq=f)
+    out, lse = bfa.fwd_chunk(qr, kc, vc, table, cu, used, max_q=100, softcap=20.0)
+    return out, lse, bfa.rope(out, p, f, inverse=True)
+
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    captured = step()
+graph.replay()
+torch.cuda.synchronize()
+eager = step()
+assert all(torch.equal(a, b) for a, b in zip(captured, eager))
+bfa.chunk_device_status()
+print("same")
+"""
+
+
+def test_the_first_calls_of_a_process_may_be_captured():
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "same" in r.stdout, r.stdout[-1000:] + r.stderr[-2000:]
+
+
+def test_a_single_kv_head_may_have_any_stride():
+    b = Batch([1, 70], [200, 333], 4, 1, 64, 16)
+    want = b.call()
+    flat_k, flat_v = b.k_cache[:, :, 0], b.v_cache[:, :, 0]
+    b.k_cache = torch.as_strided(flat_k, (*flat_k.shape[:2], 1, 64), (16 * 64, 64, 0, 1))
+    b.v_cache = torch.as_strided(flat_v, (*flat_v.shape[:2], 1, 64), (16 * 64, 64, 0, 1))
+    got = b.call()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
