@@ -477,12 +477,19 @@ def _shapes(plan, q, k, v):
     return int(B), int(q.shape[-2]), int(k.shape[-2]), int(q.shape[-1]), lse_shape
 
 
-def _result(t, like_shape, dtype, device, name):
-    """A caller's result tensor, checked, or a new one."""
+def _like(t, x, name):
+    """A caller's result tensor in the form of x, checked, or a new one."""
     if t is None:
-        return torch.empty(like_shape, dtype=dtype, device=device)
-    if t.shape != like_shape or t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must be {tuple(like_shape)} {dtype} on {device}")
+        return torch.empty_like(x)
+    return _result(t, x, x.shape, x.dtype, name)
+
+
+def _result(t, x, shape, dtype, name):
+    """A caller's result tensor, checked, or a new one beside x."""
+    if t is None:
+        return x.new_empty(shape, dtype=dtype)
+    if t.shape != shape or t.dtype is not dtype or t.device != x.device:
+        raise ValueError(f"{name} must be {tuple(shape)} {dtype} on {x.device}")
     if t.dim() and t.stride(-1) != 1:
         raise ValueError(f"the last dim of {name} must be contiguous")
     return t
@@ -496,8 +503,8 @@ def _fwd_shaped(plan, q, k, v, scale, out, return_lse, lse, stream, softcap, slo
         raise ValueError("lse must be contiguous")
 
     def body(st, finish):
-        o = _result(out, q.shape, torch.bfloat16, q.device, "out")
-        l = _result(lse, lse_shape, torch.float32, q.device, "lse") if return_lse else None
+        o = _like(out, q, "out")
+        l = _result(lse, q, lse_shape, torch.float32, "lse") if return_lse else None
         sl = None if slopes is None else slopes.contiguous()
         _lib.check(_L.bfa_fwd_shaped(plan.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), _strides_of(q),
                                      _strides_of(k), _strides_of(v), B, H, Hkv, D, scale or 0.0, cap, _addr(sl),
@@ -519,9 +526,9 @@ def _bwd_shaped(plan, q, k, v, out, dout, lse, scale, dq, dk, dv, stream, softca
     cap = _score_shape(softcap, slopes, q, H)
 
     def body(st, finish):
-        gq = _result(dq, q.shape, torch.bfloat16, q.device, "dq")
-        gk = _result(dk, k.shape, torch.bfloat16, q.device, "dk")
-        gv = _result(dv, v.shape, torch.bfloat16, q.device, "dv")
+        gq = _like(dq, q, "dq")
+        gk = _like(dk, k, "dk")
+        gv = _like(dv, v, "dv")
         l = lse.contiguous()
         sl = None if slopes is None else slopes.contiguous()
         _lib.check(_L.bfa_bwd_shaped(plan.handle, q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
@@ -682,9 +689,9 @@ def fwd_chunk(q, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, *, max_
     def body(st, finish):
         table, cu, used = _int32(block_table), _int32(cu_seqlens_q), _int32(seqused_k)
         sl = None if slopes is None else slopes.contiguous()
-        o = _result(out, q.shape, torch.bfloat16, q.device, "out")
-        l = _result(lse, (H, T), torch.float32, q.device, "lse") if return_lse else None
-        ws = torch.empty(need, dtype=torch.uint8, device=q.device) if workspace is None else workspace
+        o = _like(out, q, "out")
+        l = _result(lse, q, (H, T), torch.float32, "lse") if return_lse else None
+        ws = q.new_empty(need, dtype=torch.uint8) if workspace is None else workspace
         _lib.check(_L.bfa_fwd_chunk(q.data_ptr(), _strides_of(q), k_cache.data_ptr(), v_cache.data_ptr(), cache_strides,
                                     num_pages, page_size, table.data_ptr(), table.shape[1], cu.data_ptr(),
                                     used.data_ptr(), B, T, max_q, H, Hkv, D, scale or 0.0, window_left, cap, _addr(sl),
@@ -762,7 +769,7 @@ def rope(x, positions, inv_freq, *, interleaved=False, amplitude=1.0, inverse=Fa
         return out if out is not None else torch.empty_like(x)
 
     def body(st, finish):
-        y = _result(out, x.shape, torch.bfloat16, x.device, "out")
+        y = _like(out, x, "out")
         at, f = positions.contiguous(), inv_freq.contiguous()
         _lib.check(_L.bfa_rope(x.data_ptr(), _strides_of(x), y.data_ptr(), _strides_of(y), at.data_ptr(),
                                1 if at.dtype is torch.int64 else 0, S if at.dim() == 2 else 0, f.data_ptr(), rotary, B, S, H, D, 1 if interleaved else 0, amplitude,
@@ -802,7 +809,7 @@ def append_paged(k, v, k_cache, v_cache, block_table, cu_seqlens, seqused_k, *, 
     rotary = _check_frequencies(inv_freq, k)
 
     def body(st, finish):
-        qo = None if q is None else _result(q_out, q.shape, torch.bfloat16, q.device, "q_out")
+        qo = None if q is None else _like(q_out, q, "q_out")
         none3 = _Strides3(0, 0, 0)
         table, cu, used = _int32(block_table), _int32(cu_seqlens), _int32(seqused_k)
         f = None if inv_freq is None else inv_freq.contiguous()
