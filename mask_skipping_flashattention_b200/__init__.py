@@ -109,10 +109,14 @@ def _addr(t):
 _Strides3 = ctypes.c_int64 * 3
 
 
-def _strides_of(t):
-    """{batch, token, head} strides of a (B, S, H, D) or packed (T, H, D) tensor."""
-    st = t.stride()
+@functools.lru_cache(maxsize=4096)
+def _strides3_of(st):
     return _Strides3(st[0], st[1], st[2]) if len(st) == 4 else _Strides3(0, st[0], st[1])
+
+
+def _strides_of(t):
+    """{batch, token, head} strides of a (B, S, H, D) or packed (T, H, D) tensor (read-only)."""
+    return _strides3_of(t.stride())
 
 
 def _score_shape(softcap, slopes, q, H):
