@@ -301,11 +301,14 @@ bfa_status bfa_bwd(const bfa_plan* plan, const void* q, const void* k, const voi
  * positions i, j local to the sequence, as the plan counts them (a key at the
  * query's own position is at distance 0).
  *   softcap: 0 for none, else in [1e-3, 1e6].  slopes: device f32 [H], one per
- *   query head (any finite values), or NULL for no distance penalty.  With
- *   softcap 0 and slopes NULL they are bfa_fwd and bfa_bwd.
+ *   query head (of any sign; slope times distance must stay a finite f32), or NULL
+ *   for no distance penalty.  With softcap 0 and slopes NULL they are bfa_fwd and
+ *   bfa_bwd.
  * The backward takes the same shape as the forward whose out and lse it is given;
  * the score gradient carries the cap's factor 1 - tanh^2; slopes are constants (no
- * gradient).  Document, prefix, window and every other mask come from the plan;
+ * gradient).  Where the longest key range is at most 16 tiles, D of rows of one or two
+ * key tiles is summed from the scores instead of dO . O (the bf16 output's rounding is
+ * most of the gradient's error in short rows).  Document, prefix, window and every other mask come from the plan;
  * plans with GQA-packed tiles (bfa_plan_bsr_packed) are BFA_ERR_UNSUPPORTED (their
  * tiles mix heads: plan the routing with bfa_plan_bsr), and so is a tensor that
  * repeats its data along an axis (stride 0).  Keys and values that nothing attends

@@ -18,6 +18,9 @@
 //   - value rows outside the unit's keys (the rest of the last page, the keys before a
 //     window) are zeroed in shared memory before the product reads them, since a
 //     weight of 0 does not cancel a NaN there; scores of such keys are masked.
+// Measured: 2048 new tokens behind 14336, 32 / 8 heads, D 128, 425 us with the join = 1212
+// TFLOP/s (0.73 of the measured peak; tensor pipe 58 % active, exponentials 58 %); a step of
+// two slots takes 1.9 us, starting and ending a piece some 6.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -84,7 +87,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   grid_trigger();  // the row kernel, or the join, may take the place of blocks that are done
   // warp 3 walks this block's share of the line, a piece ahead of the others
-  Walk walk;
+  Walk walk, first_at;
+  Line first_line;
   int64_t left = 0;
   bool more = false;
   auto post_piece = [&](TileWork& w) {
@@ -105,11 +109,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   };
   if (warp == 3) {
     const Line ln = line_of<kUnitRows, kTile>(p);
-    const int64_t pos = ln.share * blockIdx.x;
-    left = min(ln.share, ln.total - pos);
+    const int64_t pos = ln.start(blockIdx.x);
+    left = ln.start(blockIdx.x + 1) - pos;
     more = left > 0;
     if (more) walk = walk_to<kUnitRows, kTile>(p, pos);
-    if (lane == 0) note_cut(p, walk, ln.share, blockIdx.x, more);
+    first_at = walk;
+    first_line = ln;
     post_piece(wk_s[0]);
   }
   if (threadIdx.x == 0) {
@@ -122,6 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_relinquish();
   }
   meet();
+  if (warp == 3 && lane == 0) note_cut(p, first_at, first_line, blockIdx.x, wk_s[0].have);
   const uint32_t tmem = tmem_slot;
   const uint64_t cap = p.wait_ns;
   // what the barriers have seen before this piece: pieces with tiles, tiles (F), commits of E,
@@ -356,12 +362,20 @@ __global__ void __launch_bounds__(kThreads, 1)
           tmem_wait_ld();
           reg_fence(sr);
           float* s = reinterpret_cast<float*>(sr);
-          if constexpr (kScore != 0) shape_row<kScore>(s, p.score, p.scale_log2, slope, pos - k0);
+          if constexpr (kScore != 0) shape_row<kScore>(s, p.score, p.scale_log2, slope, pos - k0, true);
           if (k0 < all_lo || k0 + kTile > all_hi) {
-            const int a = lo - k0, z = hi - k0;
+            // keys [lo, hi) of the row as attend-bits, 32 to a word
+            uint32_t am[4];
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+              const int a = lo - k0 - 32 * w, z = hi - k0 - 32 * w;
+              const uint32_t from = a <= 0 ? 0xffffffffu : (a > 31 ? 0u : ~((1u << a) - 1u));
+              const uint32_t to = z >= 32 ? 0xffffffffu : (z <= 0 ? 0u : ((1u << z) - 1u));
+              am[w] = from & to;
+            }
 #pragma unroll
             for (int j = 0; j < 128; ++j)
-              if (j < a || j >= z) s[j] = -INFINITY;
+              if (!((am[j >> 5] >> (j & 31)) & 1u)) s[j] = -INFINITY;
           }
           float mx8[8];
 #pragma unroll

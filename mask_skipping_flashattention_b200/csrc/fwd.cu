@@ -414,6 +414,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float c = kScore ? 1.f : p.scale_log2;
       float slope = 0.f;
       if constexpr ((kScore & kScoreSlopes) != 0) slope = __ldg(p.score.slopes + (slot ? wk.h[1] : wk.h[0])) * kLog2e;
+      const bool causal = kScore != 0 && p.plan.mask_mode == MASK_POS && p.plan.causal;
+      (void)causal;
       float m = -INFINITY, l = 0.f;
       bool ok = true;
       int kt_next = n > 0 ? p.plan.kv_tile[e0] : 0;
@@ -446,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
         reg_fence(sr);
         float* s = reinterpret_cast<float*>(sr);
-        if constexpr (kScore != 0) shape_row<kScore>(s, p.score, p.scale_log2, slope, qpos - kt * kTile);
+        if constexpr (kScore != 0) shape_row<kScore>(s, p.score, p.scale_log2, slope, qpos - kt * kTile, causal);
         if (masked) {
 #pragma unroll
           for (int j = 0; j < 128; ++j)

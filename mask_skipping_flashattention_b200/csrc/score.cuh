@@ -135,6 +135,19 @@ __device__ __forceinline__ ScoreBias score_bias(float slope, int d0, int step) {
   return r;
 }
 
+// The same where every attended entry of a row lies at or before the query (step -1, d0 - j
+// >= 0): linear everywhere, and what it gives the masked entries does not matter.
+__device__ __forceinline__ ScoreBias score_bias_causal(float slope, int d0) {
+  ScoreBias r;
+  r.slope = slope;
+  r.d0 = static_cast<float>(d0);
+  r.step = -1.f;
+  r.linear = true;
+  r.a = -slope * r.d0;
+  r.b = slope;
+  return r;
+}
+
 __device__ __forceinline__ float bias_at(const ScoreBias& r, int j) {
   return -r.slope * fabsf(fmaf(r.step, static_cast<float>(j), r.d0));
 }
@@ -165,12 +178,13 @@ __device__ __forceinline__ void shape_row_as(float* s, const ScoreParams& sp, fl
 }
 
 // A row of 128 products s becomes shaped scores in log2 units, in place (the
-// forward: one row a thread).  Called by whole warps.
+// forward: one row a thread; `causal`: no later key is attended).  Called by whole warps.
 template <int kMode>
-__device__ __forceinline__ void shape_row(float* s, const ScoreParams& sp, float scale_log2, float slope, int d0) {
+__device__ __forceinline__ void shape_row(float* s, const ScoreParams& sp, float scale_log2, float slope, int d0,
+                                          bool causal) {
   ScoreBias r = {};
   r.linear = true;
-  if (kMode & kScoreSlopes) r = score_bias(slope, d0, -1);
+  if (kMode & kScoreSlopes) r = causal ? score_bias_causal(slope, d0) : score_bias(slope, d0, -1);
   if (!(kMode & kScoreCap)) {
     if (r.linear) shape_row_as<kMode, kCapPoly, false>(s, sp, scale_log2, r);
     else shape_row_as<kMode, kCapPoly, true>(s, sp, scale_log2, r);
