@@ -1596,10 +1596,16 @@ bfa_status check_cache(const void* k_cache, const void* v_cache, const int64_t* 
 }
 
 // The kernels of a chunk call.  Sequences with up to 16 query rows a kv head (one
-// unit of the row kernel) go to the row kernel, longer ones to the tile kernel: at
-// 16 rows the row kernel takes 58 us against 63 on 8 sequences of 4096 keys (8 kv
-// heads, D 128), at 32 rows 88 against 67.  A call whose max_q rules one of them
-// out launches only the other, which then serves every sequence.
+// unit of the row kernel) go to the row kernel, longer ones to the tile kernel.
+// Measured, row against tile kernel (sequences of 4096 keys, 8 kv heads, D 128):
+//   16 rows: 8 sequences 34 / 53 us, 32 sequences  93 / 126 us
+//   32 rows: 8 sequences 45 / 53 us, 32 sequences 172 / 128 us
+//   64 rows: 8 sequences 71 / 54 us, 32 sequences 332 / 130 us
+// At 32 rows each key is read by two units, which pays only while L2 holds the
+// batch's keys; the host does not know their lengths, so the limit stays at one unit
+// (that costs the 8 sequences 8 us and saves the 32 sequences 44).  A call whose
+// max_q rules one of the kernels out launches only the other, which then serves
+// every sequence.
 struct ChunkPart {
   int rows = 0;  // rows of a unit (0: not launched)
   int slots = 0, min_share = 0, start_cost = 0;

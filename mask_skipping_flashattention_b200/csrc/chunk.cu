@@ -12,8 +12,8 @@
 // between them until they are merged at the end; both products run on
 // mma.sync m16n8k16 (bf16, fp32 sums), which at 16 rows is far from its limit.
 // Cut units leave unnormalised fp32 sums, joined by k_chunk_join.
-// Measured, 32 / 8 heads, D 128: 64 sequences of up to 8192 keys 165 us for the 1.074 GB of
-// their keys and values (6.5 TB/s, 0.99 of the measured copy rate; 3 stages of 16 keys
+// Measured, 32 / 8 heads, D 128: 64 sequences of up to 8192 keys 170 us for the 1.074 GB of
+// their keys and values (6.3 TB/s, 0.96 of the measured copy rate; 3 stages of 16 keys
 // a warp and two blocks a SM keep 128 KB in flight); one sequence of 500 keys 9 us with
 // the join, which is the latency of two launches, three dependent reads and the merge.
 #include <cstdint>

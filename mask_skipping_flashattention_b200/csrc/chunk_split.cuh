@@ -12,9 +12,10 @@
 // inside the unit, 2 b + 1 if it starts it; and block b leaves a note of the cut in
 // front of it, by which the join finds what to do.
 // Measured on single tokens (32 / 8 heads, D 128): 64 ragged sequences of up to 8192 keys
-// 168 us (0.97 of the measured copy rate), one of 32768 keys 32 us.  Before, with blocks that
-// each looked up one of many pieces: a fixed number of pieces took 178 and 88 us, and a
-// length chosen by a cost model 203 and 46 us (every block paid for the search).
+// 170 us (0.96 of the measured copy rate), one of 32768 keys 34 us.  Before, with blocks that
+// each looked up one of many pieces, no fixed number served both: 2 a SM took 199 and 40 us,
+// 3 took 178 and 50, 8 took 178 and 88; a length chosen by a cost model took 203 and 46
+// (every block paid for the search).
 //
 // The order along a unit's line only has to be the same everywhere, so lengths are a
 // closed form of the row tile (line_before) and a cut at x of w falls on key tile

@@ -12,7 +12,7 @@
 // all heads.  A thread owns one chunk pair of a head (two 16-byte chunks, 8 pairs) or
 // one chunk that is copied, in every kHeadLanes-th head: neighbouring threads cover
 // kHeadLanes whole heads (1 KB at D 128), and a batch of heads is loaded before the first is
-// stored.  Measured: 268 MB (4 x 4096 x 32 x 128) 44 us, 0.92 of the measured copy rate (54 us
+// stored.  Measured: 268 MB (4 x 4096 x 32 x 128) 44.8 us, 0.91 of the measured copy rate (54 us
 // with a thread's heads side by side and the angles computed by every thread).
 #include <cstdint>
 #include <cuda_bf16.h>
