@@ -77,10 +77,18 @@ __device__ __forceinline__ uint64_t f2_both(float c) {
   return r;
 }
 
-// any x (infinities give the cap; NaN comes out as a cap, which only masked scores may be)
+// x cut to |x| <= m; NaN stays NaN (fminf and fmaxf would make it a cap, and a row that
+// attends it a finite one)
+__device__ __forceinline__ float clamp_nan(float x, float m) {
+  float y;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(-m));
+  asm("min.NaN.f32 %0, %0, %1;" : "+f"(y) : "f"(m));
+  return y;
+}
+
+// any x (infinities give the cap)
 __device__ __forceinline__ uint64_t capped_any2(float s0, float s1, const ScoreParams& sp) {
-  const float x0 = fminf(fmaxf(s0 * sp.c0, -kTanhAnyMax), kTanhAnyMax);
-  const float x1 = fminf(fmaxf(s1 * sp.c0, -kTanhAnyMax), kTanhAnyMax);
+  const float x0 = clamp_nan(s0 * sp.c0, kTanhAnyMax), x1 = clamp_nan(s1 * sp.c0, kTanhAnyMax);
   const uint64_t x = ptx::f2_pack(x0, x1), u = ptx::f2_mul(x, x);
   uint64_t p = f2_both(1.3353410699e-08f), q = f2_both(7.7760461556e-07f);
   p = ptx::f2_fma(p, u, f2_both(2.0608182991e-05f));

@@ -362,3 +362,16 @@ def test_a_single_kv_head_may_have_any_stride():
     b.v_cache = torch.as_strided(flat_v, (*flat_v.shape[:2], 1, 64), (16 * 64, 64, 0, 1))
     got = b.call()
     assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+@pytest.mark.parametrize("by", [1.0, 80.0])  # scores inside the polynomials' range, and far past it
+@pytest.mark.parametrize("cap,with_slopes", [(None, False), (30.0, False), (30.0, True)])
+def test_nan_in_a_query_reaches_its_row_alone(by, cap, with_slopes):
+    for n in (1, 150):  # row kernel, tile kernel
+        b = Batch([n, n], [200, 201], 4, 2, 64, 16, by=by)
+        b.q[n + n // 2, 1, 7] = float("nan")
+        out, _ = b.call(softcap=cap, slopes=_slopes(4) if with_slopes else None)
+        nan = out.isnan()
+        want = torch.zeros(2 * n, 4, dtype=torch.bool, device="cuda")
+        want[n + n // 2, 1] = True
+        assert torch.equal(nan.all(-1), want) and torch.equal(nan.any(-1), want)

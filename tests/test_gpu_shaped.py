@@ -291,3 +291,21 @@ def test_repeated_data_is_refused():
     with pytest.raises(bfa.BfaError) as e:
         bfa.bwd(plan, q, k, v, out, dout[:, :1].expand(2, S, H, D), lse, softcap=9.0)
     assert e.value.status == "BFA_ERR_UNSUPPORTED"
+
+
+@pytest.mark.parametrize("by", [1.0, 80.0])  # scores inside the polynomials' range, and far past it
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cap,with_slopes", SHAPES)
+def test_nan_reaches_every_row_that_attends_it(by, D, cap, with_slopes):
+    S, H, row, key = 200, 2, 70, 150
+    q, k, v, _ = _inputs(1, S, S, H, H, D, 31, by)
+    slopes = _slopes(H) if with_slopes else None
+    plan = bfa.plan_blockids(B=1, Sq=S, Sk=S)
+    q[0, row, 0, 3] = float("nan")
+    k[0, key, 1, 5] = float("nan")
+    out, _ = bfa.fwd(plan, q, k, v, softcap=cap, slopes=slopes)
+    nan = out[0].isnan()
+    want = torch.zeros(S, H, dtype=torch.bool, device="cuda")
+    want[row, 0] = True
+    want[key:, 1] = True  # causal: the rows from the key on
+    assert torch.equal(nan.all(-1), want) and torch.equal(nan.any(-1), want)
