@@ -308,12 +308,12 @@ bfa_status bfa_bwd(const bfa_plan* plan, const void* q, const void* k, const voi
  * the score gradient carries the cap's factor 1 - tanh^2; slopes are constants (no
  * gradient).  Where the longest key range is at most 16 tiles, D of rows of one or two
  * key tiles is summed from the scores instead of dO . O (the bf16 output's rounding is
- * most of the gradient's error in short rows).  Document, prefix, window and every other mask come from the plan;
- * plans with GQA-packed tiles (bfa_plan_bsr_packed) are BFA_ERR_UNSUPPORTED (their
- * tiles mix heads: plan the routing with bfa_plan_bsr), and so is a tensor that
- * repeats its data along an axis (stride 0).  Keys and values that nothing attends
- * are multiplied by weights of 0, so they must be finite.  Everything else as for
- * bfa_fwd and bfa_bwd.
+ * most of the gradient's error in short rows).
+ * Document, prefix, window and every other mask come from the plan; plans with GQA-
+ * packed tiles (bfa_plan_bsr_packed) are BFA_ERR_UNSUPPORTED (their tiles mix heads:
+ * plan the routing with bfa_plan_bsr), and so is a tensor that repeats its data along
+ * an axis (stride 0).  Keys and values that nothing attends are multiplied by weights
+ * of 0, so they must be finite.  Everything else as for bfa_fwd and bfa_bwd.
  */
 bfa_status bfa_fwd_shaped(const bfa_plan* plan, const void* q, const void* k, const void* v,
                           const int64_t q_strides[3], const int64_t k_strides[3], const int64_t v_strides[3],
@@ -365,7 +365,8 @@ bfa_status bfa_fwd_paged(const bfa_plan* plan, const void* q, const int64_t q_st
 /*
  * Attention of the newest tokens of each sequence over a paged cache, without a
  * plan: single tokens (decoding), chunks of a prompt, or both in one batch.
- *   q, out: bf16 [total_q, H, D] packed, strides {unused, token, head}; sequence s
+ *   q, out: bf16 [total_q, H, D] packed, strides {unused, token, head} (out's not 0
+ *   where its axis has more than one entry); sequence s
  *   owns rows cu_seqlens_q[s] .. cu_seqlens_q[s + 1] (device i32 [B + 1], starting
  *   at 0).  Rows behind the last sequence are left as they are, in out and lse.
  *   seqused_k: device i32 [B], keys of each sequence in the cache, the new tokens'
@@ -407,12 +408,12 @@ bfa_status bfa_chunk_device_status(void* stream);
  * Rotary positions: pair (a, b) of a head at position n becomes
  *   (amplitude * (a cos - b sin), amplitude * (a sin + b cos)),  angle n * inv_freq[i].
  *   x, out: bf16 [B, S, H, D] (strides {batch, token, head}; packed [T, H, D] is
- *   B = 1, S = T); out may be x itself.  inv_freq: device f64 [rotary / 2], radians
- *   per position.  rotary: leading values of each head that turn, a multiple of 16
- *   up to D; the rest is copied.  interleaved: pairs (2i, 2i + 1), else
- *   (i, i + rotary / 2).  positions: device i32, or i64 with positions64, at
- *   b * positions_batch_stride + s (stride 0: the same for every batch row); any
- *   values, the angle is reduced in double.
+ *   B = 1, S = T); out may be x itself, and repeats no axis (stride 0).  inv_freq:
+ *   device f64 [rotary / 2], radians per position.  rotary: leading values of each
+ *   head that turn, a multiple of 16 up to D; the rest is copied.  interleaved:
+ *   pairs (2i, 2i + 1), else (i, i + rotary / 2).  positions: device i32, or i64
+ *   with positions64, at b * positions_batch_stride + s (stride 0: the same for
+ *   every batch row); any values, the angle is reduced in double.
  *   inverse: the rotation by -angle (same amplitude), which is the gradient:
  *   dx = bfa_rope(dout, inverse).
  * Stream-ordered, no synchronisation.
@@ -430,10 +431,10 @@ bfa_status bfa_rope(const void* x, const int64_t x_strides[3], void* out, const 
  *   seqused_k - n + t, in the place that block_table gives (caches and table as for
  *   bfa_fwd_chunk).  k turns by bfa_rope at that position (rotary 0: copied).
  *   q [total, H, D], q_out: turned the same way in the same launch, or q NULL; q_out
- *   may be q.  Tokens behind the last sequence are left out (their rows of q_out
- *   stay as they are); tokens whose place does not exist (a position below 0 or
- *   beyond pages_per_seq * page_size, a page id outside [0, num_pages)) are not
- *   written.  Two tokens in one place: either may stay.
+ *   may be q, and repeats no axis (stride 0).  Tokens behind the last sequence are
+ *   left out (their rows of q_out stay as they are); tokens whose place does not
+ *   exist (a position below 0 or beyond pages_per_seq * page_size, a page id outside
+ *   [0, num_pages)) are not written.  Two tokens in one place: either may stay.
  * Stream-ordered, no synchronisation.
  */
 bfa_status bfa_append_paged(const void* k, const int64_t k_strides[3], const void* v, const int64_t v_strides[3],

@@ -1561,6 +1561,15 @@ bfa_status need_tensor(const void* p, const char* name, const int64_t* strides, 
   return BFA_OK;
 }
 
+// A result whose axis repeats its data (an expanded tensor, stride 0) would be written by
+// several threads at once.
+bfa_status check_result(const int64_t* strides, const char* name, int64_t batch, int64_t tokens, int heads) {
+  if (!strides) return fail(BFA_ERR_INVALID_ARG, "strides of %s are NULL", name);
+  if ((batch > 1 && strides[0] == 0) || (tokens > 1 && strides[1] == 0) || (heads > 1 && strides[2] == 0))
+    return fail(BFA_ERR_INVALID_ARG, "%s repeats its data along an axis (stride 0)", name);
+  return BFA_OK;
+}
+
 bfa_status check_heads(int H, int Hkv, int D) {
   if (D != 64 && D != 128) return fail(BFA_ERR_UNSUPPORTED, "head dim %d (supported: 64, 128)", D);
   if (H <= 0 || Hkv <= 0 || H % Hkv != 0)
@@ -1685,7 +1694,8 @@ BFA_API bfa_status bfa_fwd_chunk(const void* q, const int64_t qs[3], const void*
   if ((s = check_heads(H, Hkv, D)) || (s = check_softcap(softcap))) return s;
   if (window_left == 0 || window_left < -1)
     return fail(BFA_ERR_INVALID_ARG, "window_left=%d must be positive, or -1 for no window", window_left);
-  if ((s = check_cache(k_cache, v_cache, cs, Hkv, num_pages, page_size, block_table, pages_per_seq, cu_seqlens_q, seqused_k,
+  if ((s = check_result(os, "out", 1, total_q, H)) ||
+      (s = check_cache(k_cache, v_cache, cs, Hkv, num_pages, page_size, block_table, pages_per_seq, cu_seqlens_q, seqused_k,
                        B, total_q)))
     return s;
   if (total_q == 0) return BFA_OK;
@@ -1807,7 +1817,7 @@ BFA_API bfa_status bfa_rope(const void* x, const int64_t xs[3], void* out, const
   if (S == 0) return BFA_OK;
   if (S >= (int64_t(1) << 31)) return fail(BFA_ERR_CAPACITY, "%lld tokens are too many for one call", (long long)S);
   if (positions_batch_stride < 0) return fail(BFA_ERR_INVALID_ARG, "the positions' batch stride must not be negative");
-  if ((s = need_tensor(x, "x", xs, B > 1)) || (s = need_tensor(out, "out", os, B > 1)) ||
+  if ((s = check_result(os, "out", B, S, H)) || (s = need_tensor(x, "x", xs, B > 1)) || (s = need_tensor(out, "out", os, B > 1)) ||
       (s = need_here(positions, "positions")) || (s = check_rotary(inv_freq, rotary, D, amplitude, false)))
     return s;
   RopeParams p;
@@ -1846,7 +1856,7 @@ BFA_API bfa_status bfa_append_paged(const void* k, const int64_t ks[3], const vo
                                     int Hkv, int D, const double* inv_freq, int rotary, int interleaved,
                                     float amplitude, void* stream) {
   bfa_status s;
-  if ((s = check_heads(q ? H : Hkv, Hkv, D)) ||
+  if ((s = check_heads(q ? H : Hkv, Hkv, D)) || (q && (s = check_result(qos, "q_out", 1, total, H))) ||
       (s = check_cache(k_cache, v_cache, cs, Hkv, num_pages, page_size, block_table, pages_per_seq, cu_seqlens, seqused_k, B,
                        total)) ||
       (s = check_rotary(inv_freq, rotary, D, amplitude, true)))

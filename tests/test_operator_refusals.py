@@ -168,3 +168,25 @@ def test_frequencies():
                 dict(rotary=8, ramp=(0, 1, 2)), dict(rotary=8, ramp=(10, 2, 2))):
         with pytest.raises(ValueError):
             bfa.rope_frequencies(device="cpu", **bad)
+
+
+def _refused(call, status):
+    with pytest.raises(bfa.BfaError) as e:
+        call()
+    assert e.value.status == status
+
+
+def test_results_that_repeat_an_axis_are_refused():
+    k, v, bt = _cache()
+    f = torch.zeros(16, dtype=torch.float64)
+    q, kn = torch.zeros(3, 4, 64, dtype=BF), torch.zeros(3, 2, 64, dtype=BF)
+    x = torch.zeros(2, 3, 4, 64, dtype=BF)
+    at = torch.arange(3)
+    for out in (torch.zeros(1, 4, 64, dtype=BF).expand(3, 4, 64), torch.zeros(3, 1, 64, dtype=BF).expand(3, 4, 64)):
+        _refused(lambda: bfa.fwd_chunk(q, k, v, bt, CU, USED, out=out, stream=0), "BFA_ERR_INVALID_ARG")
+        _refused(lambda: bfa.append_paged(kn, kn, k, v, bt, CU, USED, q=q, q_out=out, stream=0), "BFA_ERR_INVALID_ARG")
+        _refused(lambda: bfa.rope(q, at, f, out=out, stream=0), "BFA_ERR_INVALID_ARG")
+    _refused(lambda: bfa.rope(x, at, f, out=torch.zeros(1, 3, 4, 64, dtype=BF).expand(2, 3, 4, 64), stream=0), "BFA_ERR_INVALID_ARG")
+    # an axis of one entry has no stride of its own
+    one = torch.zeros(1, 4, 64, dtype=BF)
+    _refused(lambda: bfa.rope(one, at[:1], f, out=one.clone().as_strided((1, 4, 64), (0, 64, 1)), stream=0), "BFA_ERR_NOT_DEVICE")
