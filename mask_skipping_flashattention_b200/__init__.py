@@ -680,10 +680,11 @@ def fwd_chunk(q, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, *, max_
     are left as they are in out and lse.
     """
     (num_pages, page_size, Hkv, D), cache_strides = _check_cache(k_cache, v_cache, block_table, cu_seqlens_q, seqused_k)
-    max_q, window_left = int(max_q), int(window_left)
     _check_packed(q, "q", None, D)
     _same_device(q, k_cache, workspace)
     T, H, _ = q.shape
+    # to what the library's 32-bit arguments hold, with the same meaning (2^30 keys are all of them)
+    max_q, window_left = max(0, min(int(max_q), T)), max(-2, min(int(window_left), 1 << 30))
     B = seqused_k.shape[0]
     cap = _score_shape(softcap, slopes, q, H)
     need = _chunk_workspace(T, B, max_q, H, Hkv, D)
@@ -776,8 +777,8 @@ def rope(x, positions, inv_freq, *, interleaved=False, amplitude=1.0, inverse=Fa
         y = _like(out, x, "out")
         at, f = positions.contiguous(), inv_freq.contiguous()
         _lib.check(_L.bfa_rope(x.data_ptr(), _strides_of(x), y.data_ptr(), _strides_of(y), at.data_ptr(),
-                               1 if at.dtype is torch.int64 else 0, S if at.dim() == 2 else 0, f.data_ptr(), rotary, B, S, H, D, 1 if interleaved else 0, amplitude,
-                               1 if inverse else 0, st))
+                               1 if at.dtype is torch.int64 else 0, S if at.dim() == 2 else 0, f.data_ptr(), rotary,
+                               B, S, H, D, 1 if interleaved else 0, amplitude, 1 if inverse else 0, st))
         finish(y if out is None else None)
         return y
 

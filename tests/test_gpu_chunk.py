@@ -375,3 +375,10 @@ def test_nan_in_a_query_reaches_its_row_alone(by, cap, with_slopes):
         want = torch.zeros(2 * n, 4, dtype=torch.bool, device="cuda")
         want[n + n // 2, 1] = True
         assert torch.equal(nan.all(-1), want) and torch.equal(nan.any(-1), want)
+
+
+def test_a_window_beyond_31_bits_is_no_window():
+    b = Batch([1, 3], [200, 30], 4, 2, 64, 16)
+    want = b.call()[0]
+    for w in (2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5):
+        assert torch.equal(b.call(window_left=w)[0], want)

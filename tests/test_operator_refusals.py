@@ -190,3 +190,10 @@ def test_results_that_repeat_an_axis_are_refused():
     # an axis of one entry has no stride of its own
     one = torch.zeros(1, 4, 64, dtype=BF)
     _refused(lambda: bfa.rope(one, at[:1], f, out=one.clone().as_strided((1, 4, 64), (0, 64, 1)), stream=0), "BFA_ERR_NOT_DEVICE")
+
+
+def test_windows_beyond_32_bits_do_not_wrap():
+    k, v, bt = _cache()
+    q = torch.zeros(3, 4, 64, dtype=BF)
+    _refused(lambda: bfa.fwd_chunk(q, k, v, bt, CU, USED, window_left=5 - 2 ** 32, stream=0), "BFA_ERR_INVALID_ARG")
+    _refused(lambda: bfa.fwd_chunk(q, k, v, bt, CU, USED, window_left=2 ** 32, stream=0), "BFA_ERR_NOT_DEVICE")
