@@ -1199,6 +1199,24 @@ namespace {
 // Backward: preprocess (D, LSE * log2 e) -> dQ pass over the plan's rows -> dK/dV
 // pass over its key-tile columns.  The workspace comes from the plan pool in
 // stream order and is returned after the kernels.
+// CTAs that share a column's query heads in a shaped backward: up to four, as many as keep the
+// pass within two a SM.  Few columns otherwise leave SMs idle while each walks G heads, or wait for
+// the longest; with more columns the shares' sums only add traffic.  Measured (16 query and
+// 4 kv heads, D 128, cap 30 and penalty; forward and backward of a call in 1 / 2 / 4 shares):
+//   24 columns  90 /  77 /  72 us      128 of  8 tiles 264 / 232 / 252    256 of  8 tiles 378 / 402 / 441
+//   32 (16 / 1) 470 / 315 / 250        128 of 16 tiles 417 / 321 / 340    256 of 64 tiles 1761 / 1690 / 1713
+//   188 of 47 tiles 1290 / 1080 / 1095                                    512 of 128 tiles 6069 / 6082 / 6172
+// So between one and two columns a SM two shares pay where the columns are long (32 tiles).  Three
+// shares of 4 heads are no shorter than two (641 us for 614 in four), so a count that does not
+// shorten the longest share is taken down.
+int kv_parts(int64_t columns, int64_t longest, int G) {
+  int64_t fit = 2LL * sm_count() / std::max<int64_t>(columns, 1);
+  if (fit < 2 && longest >= 32 && 4 * columns <= 7LL * sm_count()) fit = 2;
+  const int64_t parts = std::max<int64_t>(1, std::min<int64_t>({fit, 4, G}));
+  const int64_t heads = (G + parts - 1) / parts;
+  return static_cast<int>((G + heads - 1) / heads);
+}
+
 bfa_status bwd_launch_from_host(bfa_plan* P, const void* q, const void* k, const void* v, const void* out,
                                 const void* dout, const float* lse, const int64_t* qs, const int64_t* ks,
                                 const int64_t* vs, const int64_t* os, const int64_t* dos, int B, int H, int Hkv,
@@ -1315,7 +1333,11 @@ bfa_status bwd_launch_from_host(bfa_plan* P, const void* q, const void* k, const
   // D = 128 runs the fused pass, which also needs the fp32 dQ sums (D floats a row),
   // unless reproducible sums were asked for
   const bool fused = D == 128 && !g_bwd_deterministic;
-  const int64_t ws_floats = ws_rows * (2 + (fused ? D : 0));
+  p.kv_parts = 1;
+  if (p.score.mode() != kScorePlain) p.kv_parts = kv_parts(static_cast<int64_t>(n_cols) * p.rep_kv, P->max_nkt, H / Hkv);
+  const int64_t kv_floats =
+      p.kv_parts > 1 ? static_cast<int64_t>(p.kv_parts) * p.rep_kv * n_cols * (2 * D * kTile) : 0;
+  const int64_t ws_floats = ws_rows * (2 + (fused ? D : 0)) + kv_floats;
   void* ws = nullptr;
   auto cleanup = [&]() {
     if (ws) cudaFreeAsync(ws, st);
@@ -1332,6 +1354,7 @@ bfa_status bwd_launch_from_host(bfa_plan* P, const void* q, const void* k, const
     p.ws_lse2 = static_cast<float*>(ws);
     p.ws_d = p.ws_lse2 + ws_rows;
     p.dq_acc = fused ? p.ws_d + ws_rows : nullptr;
+    p.ws_kv = p.ws_d + ws_rows * (1 + (fused ? D : 0));
   }
   BFA_CUDA(launch_bwd_prep(p, st), "backward preprocess kernel");
   if (p.score.mode() != kScorePlain && P->max_nkt <= kRefineMaxTiles) {
@@ -1345,12 +1368,15 @@ bfa_status bwd_launch_from_host(bfa_plan* P, const void* q, const void* k, const
     BFA_CUDA(launch_bwd_refine(D, tq, tdo, tk, tv, p, rows * p.rep, st), "backward refine kernel");
   }
   if (fused) {
-    BFA_CUDA(launch_bwd_fused(tk, tv, tq, tdo, p, static_cast<int64_t>(n_cols) * p.rep_kv, st), "fused backward kernel");
+    BFA_CUDA(launch_bwd_fused(tk, tv, tq, tdo, p, static_cast<int64_t>(n_cols) * p.rep_kv * p.kv_parts, st),
+             "fused backward kernel");
     BFA_CUDA(launch_bwd_dq_store(p, st), "dQ store kernel");
   } else {
     BFA_CUDA(launch_bwd_dq(D, tq, tdo, tk, tv, p, static_cast<int64_t>(P->n_rows) * p.rep, st), "dQ kernel");
-    BFA_CUDA(launch_bwd_dkdv(D, tk, tv, tq, tdo, p, static_cast<int64_t>(n_cols) * p.rep_kv, st), "dK/dV kernel");
+    BFA_CUDA(launch_bwd_dkdv(D, tk, tv, tq, tdo, p, static_cast<int64_t>(n_cols) * p.rep_kv * p.kv_parts, st),
+             "dK/dV kernel");
   }
+  if (p.kv_parts > 1) BFA_CUDA(launch_bwd_kv_store(p, st), "dK/dV store kernel");
   cleanup();
   return BFA_OK;
 }

@@ -583,7 +583,45 @@ __global__ void __launch_bounds__(kDqThreads, 1)
 struct KvWork {
   GroupInfo g;
   int32_t kt, e0, nq, nh, b, hk, steps;
+  int32_t h0;          // kScore: first query head of this CTA's share
+  int64_t part_at;     // kScore, several shares: its place in ws_kv
 };
+
+// With shaped scores the query heads of a kv head may be shared between p.kv_parts CTAs, whose fp32 sums k_bwd_kv_store adds in the order of the shares.  (Plain calls keep
+// one CTA a column, and with it their results bit for bit.)
+template <int kScore>
+__device__ __forceinline__ void kv_decode(const BwdParams& p, int& i, int& jk, int& part) {
+  if constexpr (kScore != 0) {
+    int item;
+    chunked_decode(blockIdx.x, p.n_cols, static_cast<int64_t>(p.rep_kv) * p.kv_parts,
+                   static_cast<int64_t>(p.kv_chunk) * p.kv_parts, i, item);
+    jk = item / p.kv_parts;
+    part = item - jk * p.kv_parts;
+  } else {
+    chunked_decode(blockIdx.x, p.n_cols, p.rep_kv, p.kv_chunk, i, jk);
+    part = 0;
+  }
+}
+
+// A share's fp32 sums (D columns of dV or dK), one key row a thread: column-major, so that a
+// warp's 32 rows are one line.
+template <int D>
+__device__ __forceinline__ void store_part(uint32_t tAcc, bool have, float* dst) {
+#pragma unroll 1
+  for (int cc = 0; cc < D / 32; ++cc) {
+    uint32_t o[32];
+    if (have) {
+      tmem_ld_32x32b_x32(tAcc + cc * 32, o);
+      tmem_wait_ld();
+      reg_fence(o);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j) o[j] = 0u;
+    }
+#pragma unroll
+    for (int j = 0; j < 32; ++j) dst[(cc * 32 + j) * kTile] = __uint_as_float(o[j]);
+  }
+}
 
 template <int D, int kScore>
 __global__ void __launch_bounds__(kBwdThreads, 1)
@@ -615,8 +653,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     abort_flag = 0;
     for (int i = 0; i < NBAR; ++i) mbar_init(bar(i), (i >= BP1 && i <= BP2) ? 4 : 1);
     fence_barrier_init();
-    int i, jk;
-    chunked_decode(blockIdx.x, p.n_cols, p.rep_kv, p.kv_chunk, i, jk);
+    int i, jk, part;
+    kv_decode<kScore>(p, i, jk, part);
     uint32_t* const err = p.plan.err;
     (void)err;
     const int c = static_cast<int>(BFA_IDX(p.col_order[BFA_IDX(i, p.n_cols, err)], p.n_cols, err));
@@ -637,6 +675,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #endif
     w.nh = p.pack_g > 1 ? 1 : p.H / p.Hkv;  // packed tiles hold every head of the kv head
     kv_replica_bh(p, w.g, jk, w.b, w.hk);
+    if constexpr (kScore != 0) {
+      const int first = w.nh * part / p.kv_parts;  // shares of G heads, even to one
+      w.h0 = w.hk * w.nh + first;
+      w.nh = w.nh * (part + 1) / p.kv_parts - first;
+      w.part_at = ((static_cast<int64_t>(part) * p.rep_kv + jk) * p.n_cols + c) * (2 * D * kTile);
+    }
     w.steps = w.nq * w.nh;
     wk_s = w;
   }
@@ -652,7 +696,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const uint64_t cap = p.wait_ns;
   const int steps = wk.steps;
   // step s -> query head (packed plans: the base head of the kv head) and list entry
-  auto step_head = [&](int s) { return (wk.hk * wk.nh + s / wk.nq) << p.pack_shift; };
+  auto step_head = [&](int s) { return ((kScore ? wk.h0 : wk.hk * wk.nh) + s / wk.nq) << p.pack_shift; };
   auto step_entry = [&](int s) { return wk.e0 + s % wk.nq; };
 
   if (warp == 0) {
@@ -888,7 +932,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       done = !__any_sync(0xffffffffu, !got);
     }
     tc_fence_after();
-    if (done) {
+    if (done && kScore != 0 && p.kv_parts > 1) {
+      float* const part = p.ws_kv + wk.part_at + (kpos - wk.kt * kTile);
+      store_part<D>(tLane + 256, steps > 0, part);
+      store_part<D>(tLane + 256 + D, steps > 0, part + D * kTile);
+    } else if (done) {
       const bool store = kpos < wk.g.k_len;
       const int64_t tok = static_cast<int64_t>(wk.g.k_off) + kpos;
       __nv_bfloat16* dvp =
@@ -944,6 +992,7 @@ struct FCfg {
   static constexpr uint32_t kIdescQT = idesc_bf16_f32_mn(128, 128);  // A = K^T and B = dS^T, both MN-major
 };
 static_assert(FCfg::kSmemBytes <= 232448, "fused pass shared memory");
+static_assert(17 * 8 + sizeof(KvWork) <= 512, "fused pass control block");
 
 template <int kScore>
 __global__ void __launch_bounds__(kFusedThreads, 1)
@@ -982,8 +1031,8 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
     *abort_flag = 0;
     for (int i = 0; i < NBAR; ++i) mbar_init(bar(i), (i >= BP1 && i <= BP2) ? 4 : (i == BQR ? 8 : 1));
     fence_barrier_init();
-    int i, jk;
-    chunked_decode(blockIdx.x, p.n_cols, p.rep_kv, p.kv_chunk, i, jk);
+    int i, jk, part;
+    kv_decode<kScore>(p, i, jk, part);
     uint32_t* const err = p.plan.err;
     (void)err;
     const int c = static_cast<int>(BFA_IDX(p.col_order[BFA_IDX(i, p.n_cols, err)], p.n_cols, err));
@@ -1003,6 +1052,12 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
 #endif
     w.nh = p.pack_g > 1 ? 1 : p.H / p.Hkv;  // packed tiles hold every head of the kv head
     kv_replica_bh(p, w.g, jk, w.b, w.hk);
+    if constexpr (kScore != 0) {
+      const int first = w.nh * part / p.kv_parts;  // shares of G heads, even to one
+      w.h0 = w.hk * w.nh + first;
+      w.nh = w.nh * (part + 1) / p.kv_parts - first;
+      w.part_at = ((static_cast<int64_t>(part) * p.rep_kv + jk) * p.n_cols + c) * (2 * D * kTile);
+    }
     w.steps = w.nq * w.nh;
     *wk_s = w;
   }
@@ -1017,7 +1072,7 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
   const KvWork& wk = *wk_s;
   const uint64_t cap = p.wait_ns;
   const int steps = wk.steps;
-  auto step_head = [&](int s) { return (wk.hk * wk.nh + s / wk.nq) << p.pack_shift; };
+  auto step_head = [&](int s) { return ((kScore ? wk.h0 : wk.hk * wk.nh) + s / wk.nq) << p.pack_shift; };
   auto step_entry = [&](int s) { return wk.e0 + s % wk.nq; };
 
   if (warp < 4) {
@@ -1282,7 +1337,11 @@ __global__ void __launch_bounds__(kFusedThreads, 1)
       done = !__any_sync(0xffffffffu, !got);
     }
     tc_fence_after();
-    if (done) {
+    if (done && kScore != 0 && p.kv_parts > 1) {
+      float* const part = p.ws_kv + wk.part_at + (kpos - wk.kt * kTile);
+      store_part<D>(tLane + 256, steps > 0, part);
+      store_part<D>(tLane + 256 + D, steps > 0, part + D * kTile);
+    } else if (done) {
       const bool store = kpos < wk.g.k_len;
       const int64_t tok = static_cast<int64_t>(wk.g.k_off) + kpos;
       __nv_bfloat16* dvp =
@@ -1371,6 +1430,51 @@ __global__ void __launch_bounds__(128) k_bwd_dq_store(const BwdParams p) {
     o.x = pack_bf16x2(a.x * p.scale, a.y * p.scale);
     o.y = pack_bf16x2(a.z * p.scale, a.w * p.scale);
     *reinterpret_cast<uint2*>(base + tok * p.dq_ss + static_cast<int64_t>(hrow) * p.dq_sh + lane * 4) = o;
+  }
+}
+
+// dV and dK (times scale) as bf16 from the shares' sums, added in their order: a block takes 32
+// of the 2 D columns of one (column, kv replica), a warp 32 of its rows, turned in shared memory
+__global__ void __launch_bounds__(128) k_bwd_kv_store(const BwdParams p) {
+  __shared__ float turn[4][32][33];
+  const int per = p.D / 16;  // blocks a (column, replica): 2 D / 32
+  const int64_t unit = blockIdx.x / per;
+  const int d0 = static_cast<int>(blockIdx.x % per) * 32;
+  const int c = static_cast<int>(unit % p.n_cols), jk = static_cast<int>(unit / p.n_cols);
+  const int grp = p.col_group[c];
+  const GroupInfo g = p.plan.groups[grp];
+  int b, hk;
+  kv_replica_bh(p, g, jk, b, hk);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int row0 = warp * 32, key0 = (c - p.col0[grp]) * kTile + row0;
+  const int64_t pitch = static_cast<int64_t>(p.rep_kv) * p.n_cols * (2 * p.D * kTile);
+  const float* const src = p.ws_kv + unit * (2 * p.D * kTile) + static_cast<int64_t>(d0) * kTile + row0 + lane;
+  float sum[32];  // a share's loads all in flight
+#pragma unroll
+  for (int d = 0; d < 32; ++d) sum[d] = src[d * kTile];
+#pragma unroll 1
+  for (int part = 1; part < p.kv_parts; ++part) {
+    float v[32];
+#pragma unroll
+    for (int d = 0; d < 32; ++d) v[d] = src[part * pitch + d * kTile];
+#pragma unroll
+    for (int d = 0; d < 32; ++d) sum[d] += v[d];
+  }
+#pragma unroll
+  for (int d = 0; d < 32; ++d) turn[warp][d][lane] = sum[d];
+  __syncwarp();
+  const bool is_k = d0 >= p.D;
+  const float scale = is_k ? p.scale : 1.f;
+  const int64_t ss = is_k ? p.dk_ss : p.dv_ss;
+  __nv_bfloat16* const dst = (is_k ? p.dk + static_cast<int64_t>(b) * p.dk_sb + static_cast<int64_t>(hk) * p.dk_sh
+                                   : p.dv + static_cast<int64_t>(b) * p.dv_sb + static_cast<int64_t>(hk) * p.dv_sh) +
+                             (is_k ? d0 - p.D : d0) + (lane & 15) * 2;
+#pragma unroll 4
+  for (int r = lane >> 4; r < 32; r += 2) {
+    if (key0 + r >= g.k_len) break;
+    const int d = (lane & 15) * 2;
+    *reinterpret_cast<uint32_t*>(dst + (static_cast<int64_t>(g.k_off) + key0 + r) * ss) =
+        pack_bf16x2(turn[warp][d][r] * scale, turn[warp][d + 1][r] * scale);
   }
 }
 
@@ -1488,6 +1592,14 @@ cudaError_t launch_bwd_dq_store(const BwdParams& p, cudaStream_t s) {
   if (blocks <= 0) return cudaSuccess;
   if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
   k_bwd_dq_store<<<static_cast<unsigned>(blocks), 128, 0, s>>>(p);
+  return cudaGetLastError();
+}
+
+cudaError_t launch_bwd_kv_store(const BwdParams& p, cudaStream_t s) {
+  const int64_t blocks = static_cast<int64_t>(p.rep_kv) * p.n_cols * (p.D / 16);
+  if (blocks <= 0) return cudaSuccess;
+  if (blocks > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+  k_bwd_kv_store<<<static_cast<unsigned>(blocks), 128, 0, s>>>(p);
   return cudaGetLastError();
 }
 

@@ -41,6 +41,10 @@ struct BwdParams {
   // tile), D values a row; zeroed by the preprocess, summed into by every key
   // tile of the row's list, then scaled into dq.  nullptr for the two-pass form.
   float* dq_acc;
+  // shaped scores: CTAs that share the query heads of a kv head's column (at most
+  // H / Hkv), and for more than one their fp32 sums [kv_parts, rep_kv, n_cols, dV | dK column, key row]
+  int32_t kv_parts;
+  float* ws_kv;
   // GQA-packed query tiles (bfa_plan_bsr_packed): plan row t of a tile is query
   // position t >> pack_shift of head (kv head << pack_shift) + (t & (pack_g - 1));
   // Q and dO move through 5-D maps.  pack_g = 1: rows are positions of one head.
@@ -66,6 +70,8 @@ cudaError_t launch_bwd_refine(int D, const CUtensorMap& tq, const CUtensorMap& t
                               const CUtensorMap& tv, const BwdParams& p, int64_t n_work, cudaStream_t s);
 cudaError_t launch_bwd_dq(int D, const CUtensorMap& tq, const CUtensorMap& tdo, const CUtensorMap& tk,
                           const CUtensorMap& tv, const BwdParams& p, int64_t n_work, cudaStream_t s);
+// dV and dK from the shares of a column (kv_parts > 1)
+cudaError_t launch_bwd_kv_store(const BwdParams& p, cudaStream_t s);
 cudaError_t launch_bwd_dkdv(int D, const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,
                             const CUtensorMap& tdo, const BwdParams& p, int64_t n_work, cudaStream_t s);
 cudaError_t launch_bwd_fused(const CUtensorMap& tk, const CUtensorMap& tv, const CUtensorMap& tq,

@@ -15,7 +15,7 @@
 // reciprocal with these), beside the exponential of the special-function unit.
 // Which form a group of scores takes is decided by its largest magnitude, a warp at a
 // time.  Measured, causal 8192 row, 16 / 4 heads, D 128: forward 292 us without a shape, 406,
-// 473 and 716 us in the three forms; backward 1190 us in the 7 terms, 1590 in the last.  The
+// 473 and 716 us in the three forms; backward 1135 us in the 7 terms, 1478 in the last.  The
 // backward leaves the 5 terms out: each form is four times in its code, and groups
 // that alternate between three forms made it slower (1121 -> 1322 us at a cap that splits
 // them, at the step that tried it) than the two terms saved.

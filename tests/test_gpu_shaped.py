@@ -309,3 +309,34 @@ def test_nan_reaches_every_row_that_attends_it(by, D, cap, with_slopes):
     want[row, 0] = True
     want[key:, 1] = True  # causal: the rows from the key on
     assert torch.equal(nan.all(-1), want) and torch.equal(nan.any(-1), want)
+
+
+# few columns: a kv head's query heads are shared between CTAs, evenly or not
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("H,Hkv,B,S", [(2, 1, 1, 130), (3, 1, 2, 77), (5, 1, 1, 300), (16, 2, 1, 200), (8, 4, 1, 2100)])
+def test_query_heads_shared_between_blocks(D, H, Hkv, B, S):
+    q, k, v, dout = _inputs(B, S, S, H, Hkv, D, 51 + H)
+    plan = bfa.plan_blockids(B=B, Sq=S, Sk=S)
+    _check(plan, q, k, v, dout, lambda b, h: _causal(S, S), 30.0, _slopes(H))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_shared_query_heads_into_strided_results_and_empty_columns(D):
+    B, S, H, Hkv = 1, 300, 7, 1
+    q, k, v, dout = _inputs(B, S, S, H, Hkv, D, 61)
+    mask = torch.zeros(S, S, dtype=torch.bool, device="cuda")
+    mask[:, 140:200] = True  # the first and the last key tile are attended by no query
+    mask[17] = False
+    plan = bfa.plan_dense(mask)
+    out, lse = bfa.fwd(plan, q, k, v, softcap=30.0)
+    want = bfa.bwd(plan, q, k, v, out, dout, lse, softcap=30.0)
+    wide = [torch.full((B, S, 3, 2 * D), 7.0, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    dk, dv = (w[:, :, 1:2, D:] for w in wide)
+    bfa.bwd(plan, q, k, v, out, dout, lse, softcap=30.0, dk=dk, dv=dv)
+    assert torch.equal(dk, want[1]) and torch.equal(dv, want[2])  # the shares are added in one order
+    for w, name in zip(wide, ("dk", "dv")):
+        w[:, :, 1:2, D:] = 7.0
+        assert (w == 7.0).all(), name
+    for g in want[1:]:
+        assert not g[:, :140].any() and not g[:, 200:].any() and g[:, 140:200].any()
+    _check(plan, q, k, v, dout, lambda b, h: mask, 30.0, None)
