@@ -674,8 +674,8 @@ def fwd_chunk(q, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, *, max_
     to its own position, of the last ``window_left`` of them if that is positive.
     Caches and ``block_table`` as for ``fwd_paged``; ``softcap`` and ``slopes`` as for
     ``fwd``.  ``max_q``: the most new tokens of a sequence, if known (it chooses tiles,
-    1 for decoding).  ``workspace``: a CUDA tensor to use as scratch, of at least
-    ``bfa_fwd_chunk_workspace`` bytes.  Lengths stay on the device: no synchronisation,
+    1 for decoding).  ``workspace``: a contiguous CUDA tensor to use as scratch, of at
+    least ``bfa_fwd_chunk_workspace`` bytes.  Lengths stay on the device: no synchronisation,
     and a captured call follows their contents.  Rows of q behind the last sequence
     are left as they are in out and lse.
     """
@@ -690,6 +690,8 @@ def fwd_chunk(q, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, *, max_
     need = _chunk_workspace(T, B, max_q, H, Hkv, D)
     if lse is not None and return_lse and not lse.is_contiguous():
         raise ValueError("lse must be contiguous")
+    if workspace is not None and not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous: it is used as one run of bytes")
 
     def body(st, finish):
         table, cu, used = _int32(block_table), _int32(cu_seqlens_q), _int32(seqused_k)

@@ -197,3 +197,16 @@ def test_windows_beyond_32_bits_do_not_wrap():
     q = torch.zeros(3, 4, 64, dtype=BF)
     _refused(lambda: bfa.fwd_chunk(q, k, v, bt, CU, USED, window_left=5 - 2 ** 32, stream=0), "BFA_ERR_INVALID_ARG")
     _refused(lambda: bfa.fwd_chunk(q, k, v, bt, CU, USED, window_left=2 ** 32, stream=0), "BFA_ERR_NOT_DEVICE")
+
+
+def test_a_workspace_that_is_not_one_run_of_bytes_is_refused():
+    # its bytes are counted by its values, so a view with gaps or repeats has less room than it seems to
+    k, v, bt = _cache()
+    q = torch.zeros(3, 4, 64, dtype=BF)
+    need = bfa._L.bfa_fwd_chunk_workspace(3, 1, 0, 4, 2, 64)
+    for ws in (torch.zeros(need, 2, dtype=torch.uint8)[:, 0], torch.zeros(64, 128, dtype=torch.uint8)[:, :64],
+               torch.zeros(1, dtype=torch.uint8).expand(need), torch.zeros(need, dtype=torch.uint8)[::2]):
+        with pytest.raises(ValueError, match="workspace"):
+            bfa.fwd_chunk(q, k, v, bt, CU, USED, workspace=ws, stream=0)
+    _refused(lambda: bfa.fwd_chunk(q, k, v, bt, CU, USED, workspace=torch.zeros(need, dtype=torch.uint8), stream=0),
+             "BFA_ERR_NOT_DEVICE")
