@@ -254,7 +254,8 @@ bfa_status bfa_plan_block_bits(const uint32_t* block_bits, int B, int Hkv, int S
  *   scale <= 0 selects 1/sqrt(D).
  *   out: caller-owned bf16, same logical shape as q, strides o_strides.
  *   lse: caller-owned f32 or NULL; batched [B, H, Sq], packed [H, total_q],
- *   natural log.  Rows with no attended key get out = 0 and lse = -inf.
+ *   natural log.  Rows with no attended key get out = 0 and lse = -inf; a row that
+ *   attends a NaN score gets NaN in both.
  *   For dense plans B is free; otherwise B must equal the plan's batch /
  *   sequence count, and for BSR plans Hkv must equal the routing's.
  * Asynchronous: a device-side timeout is reported by bfa_plan_device_status().
@@ -376,7 +377,7 @@ bfa_status bfa_fwd_paged(const bfa_plan* plan, const void* q, const int64_t q_st
  *   with n of them stands at position seqused_k - n + t and attends keys
  *   0 <= j <= position, with window_left > 0 only position - j < window_left
  *   (-1: no window).  Rows that attend nothing (an empty cache, a position below 0)
- *   give out = 0 and lse = -inf.
+ *   give out = 0 and lse = -inf; rows that attend a NaN score, NaN in both.
  *   k_cache, v_cache, cache_strides, num_pages, page_size, block_table,
  *   pages_per_seq: as for bfa_fwd_paged.  Keys a sequence does not have, and keys
  *   no new token sees, are not looked at (NaN there does no harm); lengths beyond

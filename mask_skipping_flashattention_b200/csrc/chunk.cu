@@ -65,11 +65,6 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// final value of a row's lse from its reference maximum (log2) and sum
-__device__ __forceinline__ float lse_of(float m, float l) {
-  return l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
-}
-
 // four consecutive values of a row of the output
 __device__ __forceinline__ void store4(const ChunkParams& p, int64_t tok, int h, int col, float4 v) {
   __nv_bfloat16* o = p.out + tok * p.o_ss + static_cast<int64_t>(h) * p.o_sh + col;

@@ -484,9 +484,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const float4 v = ld_shared_f4(stg + wrow * D * 2 + ((c16 ^ (wrow & (kChunks - 1))) << 4));
               if (row_at) *(reinterpret_cast<float4*>(row_at) + c16) = v;
             }
-            if (valid && p.lse)
-              p.lse[static_cast<int64_t>(h) * p.total_q + gtok] =
-                  l > 0.f ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+            if (valid && p.lse) p.lse[static_cast<int64_t>(h) * p.total_q + gtok] = lse_of(m, l);
           } else {
             // the swizzled rows go to the workspace as they are (the join undoes it)
             fence_proxy_async_smem();

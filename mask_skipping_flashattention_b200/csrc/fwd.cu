@@ -616,7 +616,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (ok) {
         const int64_t tok = static_cast<int64_t>(wk.q_off) + prow;
         if (p.lse && store) {
-          const float lse = (l > 0.f) ? (m + __log2f(l)) * 0.69314718055994531f : -INFINITY;
+          const float lse = lse_of(m, l);
           const int64_t li = p.varlen ? static_cast<int64_t>(hrow) * p.Sq_lse + tok
                                       : (static_cast<int64_t>(wk.b) * p.H + hrow) * p.Sq_lse + prow;
           p.lse[li] = lse;

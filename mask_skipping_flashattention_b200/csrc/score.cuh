@@ -110,6 +110,13 @@ __device__ __forceinline__ float capped_any(float s, const ScoreParams& sp) {
   return a;
 }
 
+// Natural-log LSE of a row from its reference maximum (log2 units) and its sum.  Only a row
+// that attends nothing has the sum 0 and gets -inf; a NaN score makes the sum NaN, which must
+// not pass for that (l > 0 would let it): the backward reads -inf as an empty row.
+__device__ __forceinline__ float lse_of(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + __log2f(l)) * 0.69314718055994531f;
+}
+
 enum CapForm : int { kCapPoly = 0, kCapAny = 1, kCapFew = 2 };
 
 template <int kForm>

@@ -382,3 +382,19 @@ def test_a_window_beyond_31_bits_is_no_window():
     want = b.call()[0]
     for w in (2 ** 31 - 1, 2 ** 31, 2 ** 32 + 5):
         assert torch.equal(b.call(window_left=w)[0], want)
+
+
+@pytest.mark.parametrize("by", [1.0, 80.0])
+@pytest.mark.parametrize("cap,with_slopes", [(None, False), (30.0, False), (30.0, True)])
+@pytest.mark.parametrize("n,kv", [(1, 201), (1, 70001), (9, 9000), (150, 400), (150, 20001), (300, 70001)])
+def test_the_lse_of_a_row_that_attends_a_nan_is_nan(by, cap, with_slopes, n, kv):
+    # whole units and units in a few, in some and in hundreds of pieces, of both kernels
+    b = Batch([n, n], [n + 40, kv], 4, 2, 64, 16, by=by)
+    shape = dict(softcap=cap, slopes=_slopes(4) if with_slopes else None)
+    hk, key = 1, kv - n + n // 2  # the key of a new token: the later ones attend it
+    b.k_cache[int(b.table[1, key // 16]), key % 16, hk, 7] = float("nan")
+    out, lse = b.call(**shape)
+    bad = torch.zeros(2 * n, 4, dtype=torch.bool, device="cuda")
+    bad[n + n // 2:, 2:] = True
+    assert torch.equal(lse.isnan(), bad.t()) and torch.equal(out.isnan().any(-1), bad)
+    assert torch.isfinite(lse[~bad.t()]).all()

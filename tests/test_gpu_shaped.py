@@ -340,3 +340,48 @@ def test_shared_query_heads_into_strided_results_and_empty_columns(D):
     for g in want[1:]:
         assert not g[:, :140].any() and not g[:, 200:].any() and g[:, 140:200].any()
     _check(plan, q, k, v, dout, lambda b, h: mask, 30.0, None)
+
+
+def _nan_inputs(D, H=2, S=300):
+    q, k, v, dout = _inputs(1, S, S, H, H, D, 33)
+    return q, k, v, dout, bfa.plan_blockids(B=1, Sq=S, Sk=S)
+
+
+@pytest.mark.parametrize("two_pass", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("cap,with_slopes", SHAPES + [(None, False)])
+def test_a_nan_score_shows_in_the_lse_and_in_every_gradient(two_pass, D, cap, with_slopes):
+    # an lse of -inf is a row that attends nothing, and the backward takes it for that
+    S, H, row, key = 300, 2, 70, 200
+    q, k, v, dout, plan = _nan_inputs(D, H, S)
+    shape = dict(softcap=cap, slopes=_slopes(H) if with_slopes else None)
+    q[0, row, 0, 3] = float("nan")
+    k[0, key, 1, 5] = float("nan")
+    out, lse = bfa.fwd(plan, q, k, v, **shape)
+    bad = torch.zeros(H, S, dtype=torch.bool, device="cuda")
+    bad[0, row] = True
+    bad[1, key:] = True  # causal: the rows from the key on
+    assert torch.equal(lse[0].isnan(), bad) and torch.isfinite(lse[0][~bad]).all()
+    bfa.set_bwd_deterministic(two_pass)
+    try:
+        dq, dk, dv = bfa.bwd(plan, q, k, v, out, dout, lse, **shape)
+    finally:
+        bfa.set_bwd_deterministic(False)
+    assert torch.equal(dq[0, :, 0].isnan().all(-1), bad[0]) and torch.equal(dq[0, :, 0].isnan().any(-1), bad[0])
+    assert dq[0, key:, 1].isnan().all() and torch.isfinite(dq[0, :128, 1].float()).all()
+    # every key that such a row attends
+    assert dv[0, :row + 1, 0].isnan().all() and dk[0, :row + 1, 0].isnan().all()
+    assert dv[0, :, 1].isnan().all() and dk[0, :, 1].isnan().all()
+    # key tiles that head 0's poisoned row does not reach
+    assert torch.isfinite(dv[0, 128:, 0].float()).all() and torch.isfinite(dk[0, 128:, 0].float()).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_an_infinite_score_is_no_empty_row(D):
+    S, H, key = 300, 2, 200
+    q, k, v, dout, plan = _nan_inputs(D, H, S)
+    q[0, :, 1, 5], k[0, key, 1, 5] = 1.0, float("inf")  # a score of +inf in head 1
+    lse = bfa.fwd(plan, q, k, v, slopes=_slopes(H))[1]
+    assert not torch.isneginf(lse).any()
+    assert torch.isfinite(lse[0, 0]).all() and torch.isfinite(lse[0, 1, :key]).all()
+    assert not torch.isfinite(lse[0, 1, key:]).any()
