@@ -307,11 +307,12 @@ bfa_status bfa_bwd(const bfa_plan* plan, const void* q, const void* k, const voi
  *   bfa_bwd.
  * The backward takes the same shape as the forward whose out and lse it is given;
  * the score gradient carries the cap's factor 1 - tanh^2; slopes are constants (no
- * gradient).  Where the longest key range is at most 16 tiles, D of rows of one or two
- * key tiles is summed from the scores instead of dO . O (the bf16 output's rounding is
- * most of the gradient's error in short rows).  With few key-tile columns (up to 1.75 an
- * SM) the query heads of a kv head are shared between blocks, whose fp32 dK and dV sums
- * add up to 70 MB to the workspace and are added in a fixed order.
+ * gradient).  D of rows of one or two key tiles is summed from the scores instead of
+ * dO . O (the bf16 output's rounding is most of the gradient's error in short rows),
+ * but for the first rows of causal sequences of more than 16 key tiles.
+ * With few key-tile columns (up to 1.75 an SM) the query heads of a kv head are shared
+ * between blocks, whose fp32 dK and dV sums add up to 70 MB to the workspace and are
+ * added in a fixed order.
  * Document, prefix, window and every other mask come from the plan; plans with GQA-
  * packed tiles (bfa_plan_bsr_packed) are BFA_ERR_UNSUPPORTED (their tiles mix heads:
  * plan the routing with bfa_plan_bsr), and so is a tensor that repeats its data along

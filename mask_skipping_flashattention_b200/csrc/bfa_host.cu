@@ -380,6 +380,36 @@ bfa_status build_rows(bfa_plan* P, int part_is_pos = 0) {
   return e == cudaSuccess ? BFA_OK : cuda_fail(e, "plan rows kernel");
 }
 
+// The refinement of D (k_bwd_refine): most key tiles of a group whose rows it looks at, and how
+// many of the plan's rows, the last of its order, may be short.  Known for positions, where
+// a query tile's keys are one range; every row under another mask, whose lists only the device
+// has.
+int plan_refine_nkt(const bfa_plan* P) {
+  const bool all_short = P->window > 0 && P->window <= kTile + 1;
+  return P->kind == BFA_PLAN_POSITIONAL && !all_short ? kRefineMaxTiles : INT32_MAX;
+}
+
+int64_t plan_refine_rows(const bfa_plan* P) {
+  if (P->kind != BFA_PLAN_POSITIONAL) return P->n_rows;
+  const int most = plan_refine_nkt(P);
+  int64_t rows = 0;
+  bool any = false;
+  for (const auto& g : P->groups_h) {
+    any = any || g.nkt <= most;
+    if (g.nkt <= kRefineTiles) {
+      rows += g.nqt;
+      continue;
+    }
+    for (int i = 0; i < g.nqt; ++i) {
+      if (i >= kRefineTiles && P->window < 0) break;  // causal: query tile i lists min(i + 1, nkt)
+      const int64_t first = P->window < 0 ? 0 : std::max<int64_t>(0, static_cast<int64_t>(i) * kTile - P->window + 1);
+      const int last = std::min(std::min((i + 1) * kTile, g.q_len), g.k_len) - 1;
+      if (last < first || last / kTile - first / kTile < kRefineTiles) ++rows;
+    }
+  }
+  return any ? rows : 0;
+}
+
 // Key-tile columns of the plan: every group's key tiles, groups in order.
 int plan_n_cols(const bfa_plan* P) {
   if (P->regular) return P->groups_h.empty() ? 0 : P->n_groups * P->groups_h[0].nkt;
@@ -1357,15 +1387,10 @@ bfa_status bwd_launch_from_host(bfa_plan* P, const void* q, const void* k, const
     p.ws_kv = p.ws_d + ws_rows * (1 + (fused ? D : 0));
   }
   BFA_CUDA(launch_bwd_prep(p, st), "backward preprocess kernel");
-  if (p.score.mode() != kScorePlain && P->max_nkt <= kRefineMaxTiles) {
-    // rows of few tiles there can be: the first query tiles of each group under a causal
-    // order, any under another mask
-    int64_t rows = P->n_rows;
-    if (P->kind == BFA_PLAN_POSITIONAL && P->window < 0 && !P->groups_h.empty()) {
-      rows = 0;
-      for (const auto& g : P->groups_h) rows += g.nkt <= kRefineTiles ? g.nqt : std::min(g.nqt, kRefineTiles);
-    }
-    BFA_CUDA(launch_bwd_refine(D, tq, tdo, tk, tv, p, rows * p.rep, st), "backward refine kernel");
+  if (p.score.mode() != kScorePlain) {
+    p.refine_nkt = plan_refine_nkt(P);
+    BFA_CUDA(launch_bwd_refine(D, tq, tdo, tk, tv, p, plan_refine_rows(P) * p.rep, sm_count(), st),
+             "backward refine kernel");
   }
   if (fused) {
     BFA_CUDA(launch_bwd_fused(tk, tv, tq, tdo, p, static_cast<int64_t>(n_cols) * p.rep_kv * p.kv_parts, st),

@@ -282,12 +282,17 @@ constexpr int kDqThreads = 384;
 // attends few keys has dP - D near 0 wherever its weight is near 1, so there the error is the
 // gradient's: documents of some 20 tokens with a cap had dQ and dK off by 0.0056 (2-norm),
 // 0.0037 refined; rounding alone gives 0.002.  Rows of up to kRefineTiles key tiles are
-// refined, in calls whose longest row has kRefineMaxTiles (longer rows average the error
-// out, 0.004 at 64 tiles, and refining the few short ones among them changes nothing).
+// refined.  Left out are the first rows of a causal sequence of more than kRefineMaxTiles
+// tiles: its longer rows average the error out (0.004 at 64 tiles, refined or not), and the
+// launch took 20 us of an 8192 row's 1250.  That goes by the sequence, so that no gradient
+// depends on the neighbours' lengths.
+// `item` is the (row, replica) in the order of k_bwd_dq or, with kRefine, of k_bwd_refine
+// (which holds the tensor memory over its rows); returns the row's listed tiles (the same for
+// every thread).
 template <int D, int kScore, bool kRefine>
-__global__ void __launch_bounds__(kDqThreads, 1)
-    k_bwd_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
-             const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const BwdParams p) {
+__device__ __forceinline__ int dq_row(const CUtensorMap& tmQ, const CUtensorMap& tmdO, const CUtensorMap& tmK,
+                                      const CUtensorMap& tmV, const BwdParams& p, int64_t item,
+                                      uint32_t given_tmem = 0) {
   using C = BCfg<D>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -317,11 +322,11 @@ __global__ void __launch_bounds__(kDqThreads, 1)
     for (int i = 0; i < NBAR; ++i) mbar_init(bar(i), (i == BC || i == BP || i == BP + 1) ? 8 : 1);
     fence_barrier_init();
     int i, j;
-    if constexpr (kRefine) {  // the shortest rows: the end of the order
-      i = p.plan.n_rows - 1 - static_cast<int>(blockIdx.x / static_cast<unsigned>(p.rep));
-      j = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.rep));
+    if constexpr (kRefine) {  // shortest rows first: from the end of the order
+      i = p.plan.n_rows - 1 - static_cast<int>(item / p.rep);
+      j = static_cast<int>(item % p.rep);
     } else {
-      chunked_decode(blockIdx.x, p.plan.n_rows, p.rep, p.head_chunk, i, j);
+      chunked_decode(item, p.plan.n_rows, p.rep, p.head_chunk, i, j);
     }
     uint32_t* const err = p.plan.err;
     (void)err;
@@ -349,16 +354,23 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   }
   if constexpr (kRefine) {
     __syncthreads();
-    if (wk_s.n == 0 || wk_s.n > kRefineTiles) return;
+    const int listed = wk_s.g.nkt > p.refine_nkt && wk_s.n <= kRefineTiles ? 0 : wk_s.n;
+    if (listed == 0 || listed > kRefineTiles) {
+      __syncthreads();  // every thread has read it
+      if (threadIdx.x == 0)
+        for (int i = 0; i < NBAR; ++i) mbar_inval(bar(i));
+      return listed;
+    }
+  } else {
+    if (warp == 1) {
+      tmem_alloc(smem_u32(&tmem_slot), C::kTmemCols);
+      tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
   }
-  if (warp == 1) {
-    tmem_alloc(smem_u32(&tmem_slot), C::kTmemCols);
-    tmem_relinquish();
-  }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = kRefine ? given_tmem : tmem_slot;
   const DqWork& wk = wk_s;
   const uint64_t cap = p.wait_ns;
   const int n = wk.n;
@@ -570,10 +582,47 @@ __global__ void __launch_bounds__(kDqThreads, 1)
   tc_fence_before();
   __syncthreads();
   if (abort_flag && threadIdx.x == 0) atomicOr(p.plan.err, DEVERR_TIMEOUT);
-  if (warp == 1) {
+  if constexpr (kRefine) {  // the next row takes barriers and tiles again: every copy and product has landed
+    tc_fence_after();
+    if (threadIdx.x == 0)
+      for (int i = 0; i < NBAR; ++i) mbar_inval(bar(i));
+  } else if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, C::kTmemCols);
   }
+  return n;
+}
+
+template <int D, int kScore>
+__global__ void __launch_bounds__(kDqThreads, 1)
+    k_bwd_dq(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
+             const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const BwdParams p) {
+  dq_row<D, kScore, false>(tmQ, tmdO, tmK, tmV, p, blockIdx.x);
+}
+
+// A block takes every gridDim.x-th item and ends at the first row that is too long: the host
+// knows only for positions how many rows are short, and with a block a row the others cost their
+// launches (64 x 16 rows of a windowed predicate, none short: 20 us).
+template <int D, int kScore>
+__global__ void __launch_bounds__(kDqThreads, 1)
+    k_bwd_refine(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmdO,
+                 const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV, const BwdParams p,
+                 int64_t items) {
+  constexpr uint32_t kCols = BCfg<D>::kTmemCols;
+  __shared__ uint32_t tmem_slot;
+  const int warp = threadIdx.x >> 5;
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&tmem_slot), kCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot;
+#pragma unroll 1
+  for (int64_t item = blockIdx.x; item < items; item += gridDim.x)
+    if (dq_row<D, kScore, true>(tmQ, tmdO, tmK, tmV, p, item, tmem) > kRefineTiles) break;
+  if (warp == 1) tmem_dealloc(tmem, kCols);
 }
 
 // ----------------------------------------------------------------------------
@@ -1499,13 +1548,13 @@ static cudaError_t bwd_prepare(K kernel, int smem) {
   return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
 }
 
-template <int D, int kScore, bool kRefine>
+template <int D, int kScore>
 static cudaError_t launch_dq_as(const CUtensorMap& tq, const CUtensorMap& tdo, const CUtensorMap& tk,
                                 const CUtensorMap& tv, const BwdParams& p, int64_t n_work, cudaStream_t s) {
   static DeviceOnce once;
-  const cudaError_t e = once.run([] { return bwd_prepare(k_bwd_dq<D, kScore, kRefine>, BCfg<D>::kDqSmemBytes); });
+  const cudaError_t e = once.run([] { return bwd_prepare(k_bwd_dq<D, kScore>, BCfg<D>::kDqSmemBytes); });
   if (e != cudaSuccess) return e;
-  k_bwd_dq<D, kScore, kRefine><<<static_cast<unsigned>(n_work), kDqThreads, BCfg<D>::kDqSmemBytes, s>>>(tq, tdo, tk, tv, p);
+  k_bwd_dq<D, kScore><<<static_cast<unsigned>(n_work), kDqThreads, BCfg<D>::kDqSmemBytes, s>>>(tq, tdo, tk, tv, p);
   return cudaGetLastError();
 }
 
@@ -1513,7 +1562,7 @@ template <int D>
 static cudaError_t launch_dq_one(const CUtensorMap& tq, const CUtensorMap& tdo, const CUtensorMap& tk,
                                  const CUtensorMap& tv, const BwdParams& p, int64_t n_work, cudaStream_t s) {
   return for_score_mode(p.score.mode(), [&](auto mode) {
-    return launch_dq_as<D, decltype(mode)::value, false>(tq, tdo, tk, tv, p, n_work, s);
+    return launch_dq_as<D, decltype(mode)::value>(tq, tdo, tk, tv, p, n_work, s);
   });
 }
 
@@ -1535,23 +1584,29 @@ static cudaError_t launch_dkdv_one(const CUtensorMap& tk, const CUtensorMap& tv,
   });
 }
 
-template <int D>
-static cudaError_t launch_refine_one(const CUtensorMap& tq, const CUtensorMap& tdo, const CUtensorMap& tk,
-                                     const CUtensorMap& tv, const BwdParams& p, int64_t n_work, cudaStream_t s) {
-  switch (p.score.mode()) {
-    case kScoreCap: return launch_dq_as<D, kScoreCap, true>(tq, tdo, tk, tv, p, n_work, s);
-    case kScoreSlopes: return launch_dq_as<D, kScoreSlopes, true>(tq, tdo, tk, tv, p, n_work, s);
-    case kScoreCapSlopes: return launch_dq_as<D, kScoreCapSlopes, true>(tq, tdo, tk, tv, p, n_work, s);
-    default: return cudaSuccess;  // plain scores keep the D of the preprocess
+template <int D, int kScore>
+static cudaError_t launch_refine_as(const CUtensorMap& tq, const CUtensorMap& tdo, const CUtensorMap& tk,
+                                    const CUtensorMap& tv, const BwdParams& p, int64_t items, int sms, cudaStream_t s) {
+  if constexpr (kScore == kScorePlain) {
+    return cudaSuccess;  // plain scores keep the D of the preprocess
+  } else {
+    static DeviceOnce once;
+    const cudaError_t e = once.run([] { return bwd_prepare(k_bwd_refine<D, kScore>, BCfg<D>::kDqSmemBytes); });
+    if (e != cudaSuccess) return e;
+    const unsigned blocks = static_cast<unsigned>(items < sms ? items : sms);
+    k_bwd_refine<D, kScore><<<blocks, kDqThreads, BCfg<D>::kDqSmemBytes, s>>>(tq, tdo, tk, tv, p, items);
+    return cudaGetLastError();
   }
 }
 
 cudaError_t launch_bwd_refine(int D, const CUtensorMap& tq, const CUtensorMap& tdo, const CUtensorMap& tk,
-                              const CUtensorMap& tv, const BwdParams& p, int64_t n_work, cudaStream_t s) {
-  if (n_work <= 0) return cudaSuccess;
-  if (n_work > 0x7fffffffLL) return cudaErrorInvalidConfiguration;
-  return D == 64 ? launch_refine_one<64>(tq, tdo, tk, tv, p, n_work, s)
-                 : launch_refine_one<128>(tq, tdo, tk, tv, p, n_work, s);
+                              const CUtensorMap& tv, const BwdParams& p, int64_t items, int sms, cudaStream_t s) {
+  if (items <= 0) return cudaSuccess;
+  return for_score_mode(p.score.mode(), [&](auto mode) {
+    constexpr int kMode = decltype(mode)::value;
+    return D == 64 ? launch_refine_as<64, kMode>(tq, tdo, tk, tv, p, items, sms, s)
+                   : launch_refine_as<128, kMode>(tq, tdo, tk, tv, p, items, sms, s);
+  });
 }
 
 cudaError_t launch_bwd_dq(int D, const CUtensorMap& tq, const CUtensorMap& tdo, const CUtensorMap& tk,

@@ -44,6 +44,7 @@ struct BwdParams {
   // shaped scores: CTAs that share the query heads of a kv head's column (at most
   // H / Hkv), and for more than one their fp32 sums [kv_parts, rep_kv, n_cols, dV | dK column, key row]
   int32_t kv_parts;
+  int32_t refine_nkt;  // launch_bwd_refine
   float* ws_kv;
   // GQA-packed query tiles (bfa_plan_bsr_packed): plan row t of a tile is query
   // position t >> pack_shift of head (kv head << pack_shift) + (t & (pack_g - 1));
@@ -63,11 +64,12 @@ struct BwdParams {
 };
 
 cudaError_t launch_bwd_prep(const BwdParams& p, cudaStream_t s);
-// shaped scores: D of the rows of few key tiles, from the scores (after the preprocess), for
-// the last n_work / rep rows of the plan's order
+// shaped scores: D of the rows of at most kRefineTiles key tiles, from the scores (after the
+// preprocess), among the last items / rep rows of the plan's order.  Not in groups of more than
+// refine_nkt key tiles: kRefineMaxTiles under causal positions (k_bwd_dq's comment).
 constexpr int kRefineTiles = 2, kRefineMaxTiles = 16;
 cudaError_t launch_bwd_refine(int D, const CUtensorMap& tq, const CUtensorMap& tdo, const CUtensorMap& tk,
-                              const CUtensorMap& tv, const BwdParams& p, int64_t n_work, cudaStream_t s);
+                              const CUtensorMap& tv, const BwdParams& p, int64_t items, int sms, cudaStream_t s);
 cudaError_t launch_bwd_dq(int D, const CUtensorMap& tq, const CUtensorMap& tdo, const CUtensorMap& tk,
                           const CUtensorMap& tv, const BwdParams& p, int64_t n_work, cudaStream_t s);
 // dV and dK from the shares of a column (kv_parts > 1)

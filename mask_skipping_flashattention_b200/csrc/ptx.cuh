@@ -26,6 +26,10 @@ __device__ __forceinline__ uint32_t elect_lane0() { return (threadIdx.x & 31u) =
 __device__ __forceinline__ void mbar_init(uint32_t bar, uint32_t count) {
   asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
 }
+// Before a barrier's memory is initialised again (nothing may be pending on it).
+__device__ __forceinline__ void mbar_inval(uint32_t bar) {
+  asm volatile("mbarrier.inval.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
 // Make barrier initialisation visible to the async proxy (TMA, tensor core).
 __device__ __forceinline__ void fence_barrier_init() {
   asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
