@@ -1226,27 +1226,48 @@ bfa_status fwd_checked(const bfa_plan* P, const void* q, const void* k, const vo
 
 namespace {
 
-// Backward: preprocess (D, LSE * log2 e) -> dQ pass over the plan's rows -> dK/dV
-// pass over its key-tile columns.  The workspace comes from the plan pool in
-// stream order and is returned after the kernels.
+// Longest key-tile column of the plan, in query tiles (a bound, but for positions with a window).
+int plan_longest_col(const bfa_plan* P) {
+  return P->window > 0 ? std::min(P->max_nqt, (P->window + kTile - 2) / kTile + 1) : P->max_nqt;
+}
+
 // CTAs that share a column's query heads in a shaped backward: up to four, as many as keep the
 // pass within two a SM.  Few columns otherwise leave SMs idle while each walks G heads, or wait for
-// the longest; with more columns the shares' sums only add traffic.  Measured (16 query and
-// 4 kv heads, D 128, cap 30 and penalty; forward and backward of a call in 1 / 2 / 4 shares):
-//   24 columns  90 /  77 /  72 us      128 of  8 tiles 264 / 232 / 252    256 of  8 tiles 378 / 402 / 441
-//   32 (16 / 1) 470 / 315 / 250        128 of 16 tiles 417 / 321 / 340    256 of 64 tiles 1761 / 1690 / 1713
-//   188 of 47 tiles 1290 / 1080 / 1095                                    512 of 128 tiles 6069 / 6082 / 6172
-// So between one and two columns a SM two shares pay where the columns are long (32 tiles).  Three
-// shares of 4 heads are no shorter than two (641 us for 614 in four), so a count that does not
-// shorten the longest share is taken down.
-int kv_parts(int64_t columns, int64_t longest, int G) {
+// the longest; with more columns the shares' sums only add traffic.  Measured (backward, 4 kv heads,
+// cap 30 and penalty; us in 1 / 2 / 4 shares; L: query tiles of the longest column):
+//   columns a SM      D 128, 16 query heads                      D 64
+//    64  0.4   L 16   320 / 219 / 176                            285 / 215 / 174
+//   188  1.3   L  1    97 / 107 / 140   L  2  131 / 136 / 164    174 / 180 / 195   203 / 203 / 213
+//              L  4   203 / 193 / 218   L 16  611 / 539 / 525    259 / 250 / 254   733 / 639 / 625
+//              L 47   926 / 721 / 738                            1078 / 912 / 916
+//   220  1.5   L  2   137 / 142 / 179   L  4  215 / 205 / 240    222 / 226 / 240   283 / 277 / 287
+//   256  1.7   L  8   363 / 387 / 402   L 16  672 / 696 / 673    443 / 441 / 443   819 / 820 / 811
+//              L 64, causal 1278 / 1217 / 1237                   1637 / 1589 / 1592
+//     window of 5 tiles  328 / 346 / 359   of 7  402 / 400 / 416    363 / 361 / 373   455 / 437 / 453
+//               of 3     248 / 279 / 305   of 9  475 / 451 / 469    275 / 279 / 293   543 / 514 / 523
+//   300  2.0   L 75  1657 / 1641 / 1641                          2065 / 2016 / 2003
+//   400  2.7   L 100 2794 / 2750 / 2782                          4546 / 3789 / 3634
+//   512  3.5   L 128 4396 / 4417 / 4442                          6686 / 5842 / 5737
+// So two shares also pay between one and one and a half columns a SM, where they make three
+// rounds of half the length out of two, unless a column has under four tiles; and to one and
+// three quarters where the columns are long (32 tiles, or 7, at D 64 5, of a window's equal ones).
+// The limit stays there, although D 64 would gain beyond: the sums' place grows with the columns.
+// Three shares of 4 heads are no shorter than two (641 us for 614 in four), so a count that does
+// not shorten the longest share is taken down.
+int kv_parts(const bfa_plan* P, int64_t columns, int D, int G) {
   int64_t fit = 2LL * sm_count() / std::max<int64_t>(columns, 1);
-  if (fit < 2 && longest >= 32 && 4 * columns <= 7LL * sm_count()) fit = 2;
+  const int longest = plan_longest_col(P), many = P->window > 0 ? (D == 64 ? 5 : 7) : 32;
+  if (fit < 2 && ((2 * columns <= 3LL * sm_count() && longest >= 4) ||
+                  (4 * columns <= 7LL * sm_count() && longest >= many)))
+    fit = 2;
   const int64_t parts = std::max<int64_t>(1, std::min<int64_t>({fit, 4, G}));
   const int64_t heads = (G + parts - 1) / parts;
   return static_cast<int>((G + heads - 1) / heads);
 }
 
+// Backward: preprocess (D, LSE * log2 e) -> dQ pass over the plan's rows -> dK/dV
+// pass over its key-tile columns.  The workspace comes from the plan pool in
+// stream order and is returned after the kernels.
 bfa_status bwd_launch_from_host(bfa_plan* P, const void* q, const void* k, const void* v, const void* out,
                                 const void* dout, const float* lse, const int64_t* qs, const int64_t* ks,
                                 const int64_t* vs, const int64_t* os, const int64_t* dos, int B, int H, int Hkv,
@@ -1364,7 +1385,7 @@ bfa_status bwd_launch_from_host(bfa_plan* P, const void* q, const void* k, const
   // unless reproducible sums were asked for
   const bool fused = D == 128 && !g_bwd_deterministic;
   p.kv_parts = 1;
-  if (p.score.mode() != kScorePlain) p.kv_parts = kv_parts(static_cast<int64_t>(n_cols) * p.rep_kv, P->max_nkt, H / Hkv);
+  if (p.score.mode() != kScorePlain) p.kv_parts = kv_parts(P, static_cast<int64_t>(n_cols) * p.rep_kv, D, H / Hkv);
   const int64_t kv_floats =
       p.kv_parts > 1 ? static_cast<int64_t>(p.kv_parts) * p.rep_kv * n_cols * (2 * D * kTile) : 0;
   const int64_t ws_floats = ws_rows * (2 + (fused ? D : 0)) + kv_floats;

@@ -385,3 +385,22 @@ def test_an_infinite_score_is_no_empty_row(D):
     assert not torch.isneginf(lse).any()
     assert torch.isfinite(lse[0, 0]).all() and torch.isfinite(lse[0, 1, :key]).all()
     assert not torch.isfinite(lse[0, 1, key:]).any()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("Sq,Sk,window", [(256, 8192, 0), (8192, 8192, 200)])
+def test_short_columns_are_not_shared_between_blocks(D, Sq, Sk, window):
+    # 256 columns of two or three query tiles: sharing their heads costs more than it gives.  With the
+    # batch doubled there are too many columns to share any, so equal bits are one share's order of sums
+    H, Hkv = 8, 4
+    q, k, v, dout = _inputs(1, Sq, Sk, H, Hkv, D, 141)
+    slopes, grads = _slopes(H), []
+    for B in (1, 2):
+        if window:
+            plan = bfa.plan_blockids(B=B, Sq=Sq, Sk=Sk, window_left=window)
+        else:
+            plan = bfa.plan_predicate([dict(k_lo=0)], B=B, Sq=Sq, Sk=Sk)
+        x = [t.repeat(B, 1, 1, 1) for t in (q, k, v, dout)]
+        out, lse = bfa.fwd(plan, *x[:3], softcap=30.0, slopes=slopes)
+        grads.append(bfa.bwd(plan, *x[:3], out, x[3], lse, softcap=30.0, slopes=slopes))
+    assert torch.equal(grads[0][1][0], grads[1][1][0]) and torch.equal(grads[0][2][0], grads[1][2][0])
