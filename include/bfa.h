@@ -412,12 +412,13 @@ bfa_status bfa_chunk_device_status(void* stream);
  * Rotary positions: pair (a, b) of a head at position n becomes
  *   (amplitude * (a cos - b sin), amplitude * (a sin + b cos)),  angle n * inv_freq[i].
  *   x, out: bf16 [B, S, H, D] (strides {batch, token, head}; packed [T, H, D] is
- *   B = 1, S = T); out may be x itself, and repeats no axis (stride 0).  inv_freq:
- *   device f64 [rotary / 2], radians per position.  rotary: leading values of each
- *   head that turn, a multiple of 16 up to D; the rest is copied.  interleaved:
- *   pairs (2i, 2i + 1), else (i, i + rotary / 2).  positions: device i32, or i64
- *   with positions64, at b * positions_batch_stride + s (stride 0: the same for
- *   every batch row); any values, the angle is reduced in double.
+ *   B = 1, S = T); out may be x itself, else the two share no element; it repeats
+ *   no axis (stride 0).  inv_freq: device f64 [rotary / 2], radians per position.
+ *   rotary: leading values of each head that turn, a multiple of 16 up to D; the
+ *   rest is copied.  interleaved: pairs (2i, 2i + 1), else (i, i + rotary / 2).
+ *   positions: device i32, or i64 with positions64, at b * positions_batch_stride + s
+ *   (stride 0: the same for every batch row); any values, the angle is reduced in
+ *   double.
  *   inverse: the rotation by -angle (same amplitude), which is the gradient:
  *   dx = bfa_rope(dout, inverse).
  * Stream-ordered, no synchronisation.

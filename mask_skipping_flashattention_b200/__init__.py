@@ -768,6 +768,8 @@ def rope(x, positions, inv_freq, *, interleaved=False, amplitude=1.0, inverse=Fa
     S, H, D = x.shape[-3:]
     if positions.shape not in ((S,), x.shape[:-2]):
         raise ValueError(f"positions must be {tuple(x.shape[:-2])} or {(S,)}, not {tuple(positions.shape)}")
+    if inv_freq is None:
+        raise TypeError("inv_freq is required (rope_frequencies)")
     rotary = _check_frequencies(inv_freq, x)
     _same_device(x, positions)
     if out is not None and out.data_ptr() == x.data_ptr() and out.stride() != x.stride():

@@ -210,3 +210,9 @@ def test_a_workspace_that_is_not_one_run_of_bytes_is_refused():
             bfa.fwd_chunk(q, k, v, bt, CU, USED, workspace=ws, stream=0)
     _refused(lambda: bfa.fwd_chunk(q, k, v, bt, CU, USED, workspace=torch.zeros(need, dtype=torch.uint8), stream=0),
              "BFA_ERR_NOT_DEVICE")
+
+
+def test_rope_without_frequencies_is_a_type_error():
+    x, p = torch.zeros(2, 4, 64, dtype=BF), torch.zeros(2, dtype=torch.int32)
+    with pytest.raises(TypeError, match="inv_freq"):
+        bfa.rope(x, p, None, stream=0)
