@@ -396,7 +396,9 @@ bfa_status bfa_fwd_paged(const bfa_plan* plan, const void* q, const int64_t q_st
  * Results do not depend on the order in which blocks run.  A wait that gives up
  * (bfa_set_wait_timeout_ns) is reported by bfa_chunk_device_status, which
  * synchronises `stream`, covers every chunk call on the current device since it
- * was last asked, and clears what it reports.
+ * was last asked, and clears what it reports.  In the checked build it also reports
+ * BFA_ERR_BOUNDS if an index of these kernels, of bfa_rope's or of bfa_append_paged's
+ * left its array.
  */
 int64_t bfa_fwd_chunk_workspace(int64_t total_q, int B, int max_q, int H, int Hkv, int D);
 bfa_status bfa_fwd_chunk(const void* q, const int64_t q_strides[3], const void* k_cache, const void* v_cache,

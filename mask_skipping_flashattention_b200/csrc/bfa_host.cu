@@ -1865,6 +1865,8 @@ BFA_API bfa_status bfa_chunk_device_status(void* stream) {
   BFA_CUDA(cudaStreamSynchronize(st), "chunk status");
   if (!v) return BFA_OK;
   BFA_CUDA(cudaMemsetAsync(word, 0, sizeof(v), st), "clear the chunk status");
+  if (v & DEVERR_BOUNDS)
+    return fail(BFA_ERR_BOUNDS, "checked build: an index of a chunk, rotary or append kernel left its array");
   return fail(BFA_ERR_TIMEOUT, "a chunk kernel gave up on a wait");
 }
 
@@ -1915,6 +1917,7 @@ BFA_API bfa_status bfa_rope(const void* x, const int64_t xs[3], void* out, const
   p.positions64 = positions64 ? 1 : 0;
   p.pos_sb = positions_batch_stride;
   p.page_size = 1;
+  if (kChecked && !(p.err = chunk_err_word())) return fail(BFA_ERR_CUDA, "the chunk kernels' status word has no address");
   cudaError_t e = launch_rope(p, sm_count(), static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "rotary kernel");
   return BFA_OK;
@@ -1976,6 +1979,7 @@ BFA_API bfa_status bfa_append_paged(const void* k, const int64_t ks[3], const vo
   p.page_size = page_size;
   p.pages_per_seq = pages_per_seq;
   p.block_table = block_table;
+  if (kChecked && !(p.err = chunk_err_word())) return fail(BFA_ERR_CUDA, "the chunk kernels' status word has no address");
   cudaError_t e = launch_rope(p, sm_count(), static_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "append kernel");
   return BFA_OK;

@@ -67,6 +67,7 @@ __device__ __forceinline__ void mma16816(float (&d)[4], const uint32_t (&a)[4], 
 
 // four consecutive values of a row of the output
 __device__ __forceinline__ void store4(const ChunkParams& p, int64_t tok, int h, int col, float4 v) {
+  BFA_CHECK(h >= 0 && h < p.H, p.err);
   __nv_bfloat16* o = p.out + tok * p.o_ss + static_cast<int64_t>(h) * p.o_sh + col;
   *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
@@ -133,7 +134,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) k_chunk_rows(const ChunkParams
       const int key = kb0 + t * kRowKeys + (lane & 15);
       if (t >= n || key < lo_u || key >= hi_u) return -1;
       const int pi = key / p.page_size;
-      const int64_t page = __ldg(bt + pi);
+      const int64_t page = __ldg(bt + BFA_IDX(pi, p.pages_per_seq, p.err));
       if (page < 0 || page >= p.num_pages) return -1;
       return page * p.c_sp + static_cast<int64_t>(key - pi * p.page_size) * p.c_st;
     };
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(kRowThreads, 2) k_chunk_rows(const ChunkParams
         hi[i] = in ? min(kv, pos[i] + 1) : 0;
         lo[i] = p.window >= 0 ? max(0, pos[i] - p.window + 1) : 0;
         slope[i] = (kScore && p.score.slopes) ? __ldg(p.score.slopes + h) * kLog2e : 0.f;
-        qr[i] = in ? p.q + (static_cast<int64_t>(q0) + t) * p.q_ss + static_cast<int64_t>(h) * p.q_sh : nullptr;
+        qr[i] = in ? p.q + BFA_IDX(static_cast<int64_t>(q0) + t, p.total_q, p.err) * p.q_ss + static_cast<int64_t>(h) * p.q_sh : nullptr;
       }
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
@@ -319,10 +320,10 @@ __global__ void __launch_bounds__(kRowThreads, 2) k_chunk_rows(const ChunkParams
       if (pc.whole) {
         const int t = (row0 + r) / p.G, h = pc.hk * p.G + (row0 + r) - t * p.G;
         const float inv = L > 0.f ? 1.f / L : 0.f;
-        store4(p, static_cast<int64_t>(q0) + t, h, c4, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
-        if (p.lse && c4 == 0) p.lse[static_cast<int64_t>(h) * p.total_q + q0 + t] = lse_of(M, L);
+        store4(p, BFA_IDX(static_cast<int64_t>(q0) + t, p.total_q, p.err), h, c4, make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv));
+        if (p.lse && c4 == 0) p.lse[BFA_IDX(static_cast<int64_t>(h) * p.total_q + q0 + t, static_cast<int64_t>(p.H) * p.total_q, p.err)] = lse_of(M, L);
       } else {
-        const int64_t at = static_cast<int64_t>(pc.place) * kChunkRows + r;
+        const int64_t at = BFA_IDX(static_cast<int64_t>(pc.place) * kChunkRows + r, 2LL * p.slots * kChunkRows, p.err);
         *reinterpret_cast<float4*>(p.ws_o + at * D + c4) = o;
         if (c4 == 0) p.ws_ml[at] = make_float2(M, L);
       }
@@ -351,14 +352,18 @@ struct JoinShared {
 
 template <int D, int R>
 __device__ __forceinline__ void join_cut(const ChunkParams& p, int cut, int part, int parts, JoinShared<D>* sh) {
-  const Cut c = static_cast<const Cut*>(p.ws_cuts)[cut];
+  const Cut c = static_cast<const Cut*>(p.ws_cuts)[BFA_IDX(cut, p.slots, p.err)];
   if (c.pieces == 0) return;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   constexpr int kV = D / 32;  // columns a lane
   const int row0 = c.rt * R, n = min(R, c.rows - row0), cuts = c.pieces - 1;
   const int first = cut - 1 - c.index;  // the block that starts the unit (its odd place); the others' even ones
   const int ra = n * c.index / cuts, rb = n * (c.index + 1) / cuts;
-  auto place = [&](int i, int r) { return static_cast<int64_t>(i == 0 ? 2 * first + 1 : 2 * (first + i)) * R + r; };
+  BFA_CHECK(c.index >= 0 && c.index < cuts && first >= 0 && first + cuts < p.slots && n > 0, p.err);
+  auto place = [&](int i, int r) {
+    return static_cast<int64_t>(BFA_IDX(static_cast<int64_t>(i == 0 ? 2 * first + 1 : 2 * (first + i)) * R + r,
+                                        2LL * p.slots * R, p.err));
+  };
   // the lane's columns of a workspace row; the tile kernel's rows have their 16-byte chunks
   // swizzled by the row's place among 32
   auto load = [&](int64_t at, float (&a)[kV]) {
@@ -373,7 +378,8 @@ __device__ __forceinline__ void join_cut(const ChunkParams& p, int cut, int part
   };
   auto store = [&](int r, const float (&o)[kV], float M, float L) {
     const int t = (row0 + r) / p.G, h = c.hk * p.G + (row0 + r) - t * p.G;
-    const int64_t tok = static_cast<int64_t>(c.q0) + t;
+    const int64_t tok = BFA_IDX(static_cast<int64_t>(c.q0) + t, p.total_q, p.err);
+    BFA_CHECK(h >= 0 && h < p.H, p.err);
     const float inv = L > 0.f ? 1.f / L : 0.f;
     uint32_t* dst = reinterpret_cast<uint32_t*>(p.out + tok * p.o_ss + static_cast<int64_t>(h) * p.o_sh + lane * kV);
     if constexpr (kV == 4)

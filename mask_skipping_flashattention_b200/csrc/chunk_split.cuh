@@ -25,6 +25,7 @@
 #include <cstdint>
 
 #include "chunk_params.cuh"
+#include "plan_types.cuh"
 
 namespace bfa {
 
@@ -53,8 +54,9 @@ struct Cut {
 static_assert(sizeof(Cut) == kChunkCutBytes, "workspace size");
 
 template <int R>
-__device__ __forceinline__ SeqSpan seq_span(const ChunkParams& p, int s) {
+__device__ __forceinline__ SeqSpan seq_span(const ChunkParams& p, int s0) {
   SeqSpan sp;
+  const int s = static_cast<int>(BFA_IDX(s0, p.B, p.err));
   // lengths outside their arrays are cut to them
   const int a = min(max(__ldg(p.cu_seqlens + s), 0), p.total_q);
   const int b = min(max(__ldg(p.cu_seqlens + s + 1), a), p.total_q);
@@ -211,7 +213,7 @@ __device__ __forceinline__ void note_cut(const ChunkParams& p, const Walk& k, co
     c.q0 = k.sp.q0;
     c.rows = k.sp.q_len * p.G;
   }
-  static_cast<Cut*>(p.ws_cuts)[b] = c;
+  static_cast<Cut*>(p.ws_cuts)[BFA_IDX(b, p.slots, p.err)] = c;
 }
 
 // Part [k.x, x1) of the unit at k as a piece of block b.
@@ -234,6 +236,11 @@ __device__ __forceinline__ Piece piece_of(const ChunkParams& p, const Walk& k, i
   const float step = static_cast<float>(n) / static_cast<float>(k.w);
   pc.t0 = t_lo + (k.x == 0 ? 0 : min(n, static_cast<int>(static_cast<float>(k.x) * step)));
   pc.t1 = t_lo + (x1 == k.w ? n : min(n, static_cast<int>(static_cast<float>(x1) * step)));
+  // a unit of the batch, its keys inside the table, its place inside the workspace
+  BFA_CHECK(pc.s >= 0 && pc.s < p.B && pc.hk >= 0 && pc.hk < p.Hkv && pc.rt >= 0 && row0 < rows, p.err);
+  BFA_CHECK(pc.t0 <= pc.t1 && (n == 0 || static_cast<int64_t>(pc.hi) <= static_cast<int64_t>(p.pages_per_seq) * p.page_size),
+            p.err);
+  BFA_CHECK(pc.whole || (pc.place >= 0 && pc.place < 2 * p.slots), p.err);
   return pc;
 }
 

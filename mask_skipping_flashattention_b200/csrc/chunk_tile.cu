@@ -30,6 +30,7 @@
 #include "chunk_split.cuh"
 #include "device_once.cuh"
 #include "fwd_tiles.cuh"
+#include "plan_types.cuh"
 #include "ptx.cuh"
 #include "score.cuh"
 
@@ -175,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int key = (wk.pc.t0 + j) * kTile + lane * box;
           if (lane >= boxes || j >= n || key >= wk.pc.hi || key + box <= wk.pc.lo) return past;
           const int pi = key / p.page_size;
-          const int page = __ldg(bt + pi);
+          const int page = __ldg(bt + BFA_IDX(pi, p.pages_per_seq, p.err));
           return (page < 0 || page >= p.num_pages) ? past : page * p.page_size + (key - pi * p.page_size);
         };
         auto load = [&](const CUtensorMap* map, uint8_t* dst, uint32_t b, int row) {
@@ -319,7 +320,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         constexpr int kChunks = D / 8, kPer = 32 / kChunks;  // 16-byte chunks of a row, rows an instruction
         const uint32_t tile = smem_u32(slot ? sQ1 : sQ0);
         const int c16 = lane % kChunks;
-        const __nv_bfloat16* src = p.q + (static_cast<int64_t>(wk.pc.sp.q0) + tok) * p.q_ss + static_cast<int64_t>(h) * p.q_sh;
+        const __nv_bfloat16* src = p.q + BFA_IDX(static_cast<int64_t>(wk.pc.sp.q0) + tok, p.total_q, p.err) * p.q_ss + static_cast<int64_t>(h) * p.q_sh;
         const uint64_t at = valid ? reinterpret_cast<uint64_t>(src) : 0;  // of this lane's row
 #pragma unroll
         for (int half = 0; half < 2; ++half) {
@@ -439,8 +440,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           // side meets in a bank.  Direct stores, a row a thread, took 5 us.
           const bool whole = wk.pc.whole != 0;
           const float inv = l > 0.f ? 1.f / l : 0.f;
-          const int64_t gtok = static_cast<int64_t>(wk.pc.sp.q0) + tok;
-          const int64_t wr = static_cast<int64_t>(wk.pc.place) * kUnitRows + slot * kTile + row;
+          const int64_t gtok = BFA_IDX(static_cast<int64_t>(wk.pc.sp.q0) + tok, p.total_q, p.err);
+          const int64_t wr = BFA_IDX(static_cast<int64_t>(wk.pc.place) * kUnitRows + slot * kTile + row,
+                                     2LL * p.slots * kUnitRows, p.err);
+          BFA_CHECK(h >= 0 && h < p.H, p.err);
           // this warp's 32 rows: bf16 in the slot's Q tile, fp32 in a K or V stage pair
           constexpr int kWide = D / 4;  // 16-byte chunks of an fp32 row
           const uint32_t stg = whole ? smem_u32(slot ? sQ1 : sQ0) + quarter * 32 * D * 2

@@ -18,6 +18,7 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
+#include "plan_types.cuh"
 #include "ptx.cuh"
 #include "rope_params.cuh"
 
@@ -81,7 +82,8 @@ __global__ void __launch_bounds__(kRopeThreads, kRagged ? 4 : 3) k_rope(const Ro
             pos = static_cast<int64_t>(__ldg(p.seqused_k + s)) - (end - first) + (tok - first);
             if (pos >= 0 && pos < static_cast<int64_t>(p.pages_per_seq) * p.page_size) {
               const int pi = static_cast<int>(pos) / p.page_size;
-              const int64_t page = __ldg(p.block_table + static_cast<int64_t>(s) * p.pages_per_seq + pi);
+              const int64_t page = __ldg(p.block_table + static_cast<int64_t>(s) * p.pages_per_seq +
+                                         BFA_IDX(pi, p.pages_per_seq, p.err));
               if (page >= 0 && page < p.num_pages)
                 row = page * p.c_sp + (static_cast<int>(pos) - pi * p.page_size) * p.c_st;
             }
@@ -100,13 +102,15 @@ __global__ void __launch_bounds__(kRopeThreads, kRagged ? 4 : 3) k_rope(const Ro
     const double x = static_cast<double>(pos_s[t]) * __ldg(p.inv_freq + (i - t * half)) * 0.15915494309189533577;
     float sn, cs;
     sincospif(2.f * static_cast<float>(x - rint(x)), &sn, &cs);
-    turn_s[i] = make_float2(cs * p.amplitude, sn * p.amplitude * p.sign);
+    turn_s[BFA_IDX(i, kRopePairs, p.err)] = make_float2(cs * p.amplitude, sn * p.amplitude * p.sign);
   }
   __syncthreads();
   const unsigned t = threadIdx.x / lanes, in_tok = threadIdx.x - t * lanes;
   const unsigned c = in_tok % chunks;
   if (t >= per || row_s[t] == -2) return;
   const int64_t tok = tok0 + t, row = row_s[t];
+  BFA_CHECK(tok >= 0 && tok < p.tokens && per <= kRopeTokens, p.err);
+  BFA_CHECK(row < p.num_pages * p.c_sp, p.err);
   const int64_t b = kRagged ? 0 : tok / p.S, st = tok - b * p.S;
 
   const bool turn = c < pairs;
@@ -115,6 +119,7 @@ __global__ void __launch_bounds__(kRopeThreads, kRagged ? 4 : 3) k_rope(const Ro
   if (!turn) ca = cb = p.rotary + (c - pairs) * 8;
   else if (p.interleaved) { ca = c * 16; cb = ca + 8; }
   else { ca = c * 8; cb = ca + p.rotary / 2; }
+  BFA_CHECK(ca >= 0 && ca + 8 <= p.D && cb >= 0 && cb + 8 <= p.D, p.err);
   float co[8], si[8];
   if (turn) {
     const float4* v = reinterpret_cast<const float4*>(turn_s + t * half + c * 8);

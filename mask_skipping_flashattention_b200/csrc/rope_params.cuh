@@ -42,6 +42,7 @@ struct RopeParams {
   int64_t num_pages;
   int32_t page_size, pages_per_seq;
   const int32_t* block_table;
+  uint32_t* err;  // status word of the chunk kernels (written by the checked build's index checks)
 };
 
 cudaError_t launch_rope(const RopeParams& p, int sms, cudaStream_t s);
