@@ -381,11 +381,15 @@ bfa_status bfa_fwd_paged(const bfa_plan* plan, const void* q, const int64_t q_st
  *   give out = 0 and lse = -inf; rows that attend a NaN score, NaN in both.
  *   k_cache, v_cache, cache_strides, num_pages, page_size, block_table,
  *   pages_per_seq: as for bfa_fwd_paged.  Keys a sequence does not have, and keys
- *   no new token sees, are not looked at (NaN there does no harm); lengths beyond
- *   pages_per_seq * page_size count as that; page ids outside [0, num_pages) read
- *   as keys and values of zeros.
+ *   no new token sees, are not looked at (NaN there does no harm); a NaN or infinite
+ *   value of a key that only some of a sequence's new tokens see may reach the others
+ *   too, whose weight for it is 0.  Lengths beyond pages_per_seq * page_size count as
+ *   that; page ids outside [0, num_pages) read as keys and values of zeros.
  *   max_q: the most new tokens of a sequence (0: unknown).  It only chooses the
- *   tiles: sequences beyond it are served too.
+ *   kernels: sequences beyond it are served too.  Give it for single tokens: where
+ *   total_q tokens times H / Hkv are more than 16, an unknown max_q also launches the
+ *   kernel for longer chunks, which finds nothing to do (64 sequences of 1000 keys 55
+ *   us with max_q 1 and 67 without, of 4096 keys 174 and 184).
  *   scale, softcap, slopes: as for bfa_fwd_shaped.  lse: f32 [H, total_q] or NULL.
  *   workspace: device, 16-byte aligned, at least bfa_fwd_chunk_workspace(...) bytes
  *   for the same total_q, B, max_q, H, Hkv, D; its contents need no preparation

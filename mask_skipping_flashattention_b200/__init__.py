@@ -673,9 +673,10 @@ def fwd_chunk(q, k_cache, v_cache, block_table, cu_seqlens_q, seqused_k, *, max_
     new token of a sequence stands at position seqused_k - 1; each attends the keys up
     to its own position, of the last ``window_left`` of them if that is positive.
     Caches and ``block_table`` as for ``fwd_paged``; ``softcap`` and ``slopes`` as for
-    ``fwd``.  ``max_q``: the most new tokens of a sequence, if known (it chooses tiles,
-    1 for decoding).  ``workspace``: a contiguous CUDA tensor to use as scratch, of at
-    least ``bfa_fwd_chunk_workspace`` bytes.  Lengths stay on the device: no synchronisation,
+    ``fwd``.  ``max_q``: the most new tokens of a sequence, if known: it chooses the
+    kernels, and decoding without it (1) also launches the one for longer chunks (10 us).
+    ``workspace``: a contiguous CUDA tensor to use as scratch, of at least
+    ``bfa_fwd_chunk_workspace`` bytes.  Lengths stay on the device: no synchronisation,
     and a captured call follows their contents.  Rows of q behind the last sequence
     are left as they are in out and lse.
     """

@@ -1684,9 +1684,12 @@ bfa_status check_cache(const void* k_cache, const void* v_cache, const int64_t* 
 //   64 rows: 8 sequences 71 / 54 us, 32 sequences 332 / 130 us
 // At 32 rows each key is read by two units, which pays only while L2 holds the
 // batch's keys; the host does not know their lengths, so the limit stays at one unit
-// (that costs the 8 sequences 8 us and saves the 32 sequences 44).  A call whose
-// max_q rules one of the kernels out launches only the other, which then serves
-// every sequence.
+// (that costs the 8 sequences 8 us and saves the 32 sequences 44).  Neither kernel is
+// near the bytes in between: single tokens of 64 sequences of 4096 keys with one kv head,
+// whose keys take 20.5 us to read, take 43 us with 16 query heads (row kernel), 59, 61 and
+// 64 us with 32, 64 and 128 (tile kernel; the rows up to 256 are padding).  A call whose
+// max_q rules one of the kernels out launches only the other, which then serves every
+// sequence.
 struct ChunkPart {
   int rows = 0;  // rows of a unit (0: not launched)
   int slots = 0, min_share = 0, start_cost = 0;

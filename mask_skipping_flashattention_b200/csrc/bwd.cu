@@ -636,8 +636,9 @@ struct KvWork {
   int64_t part_at;     // kScore, several shares: its place in ws_kv
 };
 
-// With shaped scores the query heads of a kv head may be shared between p.kv_parts CTAs, whose fp32 sums k_bwd_kv_store adds in the order of the shares.  (Plain calls keep
-// one CTA a column, and with it their results bit for bit.)
+// With shaped scores the query heads of a kv head may be shared between p.kv_parts CTAs, whose
+// fp32 sums k_bwd_kv_store adds in the order of the shares.  (Plain calls keep one CTA a
+// column, and with it their results bit for bit.)
 template <int kScore>
 __device__ __forceinline__ void kv_decode(const BwdParams& p, int& i, int& jk, int& part) {
   if constexpr (kScore != 0) {

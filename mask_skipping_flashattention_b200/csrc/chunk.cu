@@ -6,8 +6,8 @@
 //
 // Bound by HBM: a key and its value are 4 D bytes a kv head and meet only G query
 // heads of a token.  A block runs one piece of the keys (chunk_split.cuh) for 16
-// or 32 query rows of one kv head (rows = tokens x the G heads, so the group shares
-// every byte).  Its four warps take 16 keys of a 64-key tile each, with a ring of
+// query rows of one kv head (rows = tokens x the G heads, so the group shares every
+// byte).  Its four warps take 16 keys of a 64-key tile each, with a ring of
 // asynchronous copies of their own, their own online softmax and no barrier
 // between them until they are merged at the end; both products run on
 // mma.sync m16n8k16 (bf16, fp32 sums), which at 16 rows is far from its limit.

@@ -18,9 +18,12 @@
 //   - value rows outside the unit's keys (the rest of the last page, the keys before a
 //     window) are zeroed in shared memory before the product reads them, since a
 //     weight of 0 does not cancel a NaN there; scores of such keys are masked.
-// Measured: 2048 new tokens behind 14336, 32 / 8 heads, D 128, 421 to 425 us with the join = 1.21
-// to 1.23 PFLOP/s (0.73 of the measured peak; tensor pipe 61 % active, exponentials 61 %); a step of
-// two slots takes 2 us, a piece 2 us to its first scores and 4 to 7 us to end.
+// P is rounded to bf16 for P V, as V is given in it (at most 2^-8 of each weight; the
+// sum of the weights is taken before); statistics, sums and the parts of cut units stay in fp32.
+// Measured: 2048 new tokens behind 14336, 32 / 8 heads, D 128, 421 to 425 us with the join in a
+// burst of ten calls = 1.21 to 1.23 PFLOP/s (0.73 of the measured burst peak; tensor pipe 61 %
+// active, exponentials 61 %), 487 us in a row of calls, which the power cap slows; a step of two
+// slots takes 2 us, a piece 2 us to its first scores and 4 to 7 us to end.
 #include <cstdint>
 #include <cuda.h>
 #include <cuda_bf16.h>
